@@ -640,4 +640,228 @@ fq_status fq_requantize_transpose(const fq_desc* d, const fq_quantized* in, cons
                                         (uint8_t*)out->colwise.data, (uint8_t*)out->colwise.scale, st));
 }
 
+// ---------------------------------------------------------------- operators on 8-bit data
+static fq_status check_gemm(const fq_gemm_desc* d)
+{
+    if (!d || d->m < 0 || d->n < 0 || d->k < 0)
+        return FQ_E_INVALID;
+    if (d->out_dtype != FQ_IN_F32 && d->out_dtype != FQ_IN_BF16)
+        return FQ_E_INVALID;
+    if (d->scale_mode != FQ_SCALE_DEFAULT && d->scale_mode != FQ_SCALE_POW2)
+        return FQ_E_INVALID;
+    if (d->accumulate != 0 && d->accumulate != 1)
+        return FQ_E_INVALID;
+    if (d->b_block_rows != 1 && d->b_block_rows != 128)
+        return FQ_E_UNSUPPORTED;
+    if (d->accumulate && d->out_dtype != FQ_IN_F32)
+        return FQ_E_UNSUPPORTED;
+    if (d->k % 128 || (d->b_block_rows == 128 && d->n % 128) || d->k > (int64_t(1) << 23))
+        return FQ_E_SHAPE;
+    auto over = [](int64_t x, int64_t y) { return y > 0 && x > kMaxElems / y; };
+    if (over(d->m, d->k) || over(d->n, d->k) || over(d->m, d->n))
+        return FQ_E_SHAPE;
+    return FQ_OK;
+}
+
+static GemmArgs gemm_args(const fq_gemm_desc* d)
+{
+    GemmArgs g;
+    g.m = d->m;
+    g.n = d->n;
+    g.k = d->k;
+    g.b1 = d->b_block_rows == 1;
+    g.bf = d->out_dtype == FQ_IN_BF16;
+    g.acc = d->accumulate;
+    g.pow2 = d->scale_mode == FQ_SCALE_POW2;
+    return g;
+}
+
+fq_status fq_gemm_workspace(const fq_gemm_desc* d, size_t* bytes)
+{
+    const fq_status s = check_gemm(d);
+    if (s != FQ_OK)
+        return s;
+    if (bytes)
+        *bytes = d->m == 0 || d->n == 0 ? 0 : gemm_workspace(gemm_args(d));
+    return FQ_OK;
+}
+
+fq_status fq_gemm(const fq_gemm_desc* d, const fq_plane* a, const fq_plane* b, void* out, void* ws, size_t ws_bytes,
+                  hipStream_t st)
+{
+    const fq_status s = check_gemm(d);
+    if (s != FQ_OK)
+        return s;
+    if (!a || !b)
+        return FQ_E_INVALID;
+    if (d->m == 0 || d->n == 0)
+        return FQ_OK;
+    if (!out || (d->k > 0 && (!a->data || !a->scale || !b->data || !b->scale)))
+        return FQ_E_INVALID;
+    if (!aligned(out, 16) || !aligned(a->data, 16) || !aligned(a->scale, 16) || !aligned(b->data, 16) ||
+        !aligned(b->scale, 16))
+        return FQ_E_ALIGN;
+    GemmArgs g = gemm_args(d);
+    const size_t need = gemm_workspace(g);
+    if (need) {
+        if (!ws || ws_bytes < need)
+            return FQ_E_WORKSPACE;
+        if (!aligned(ws, 16))
+            return FQ_E_ALIGN;
+    }
+    g.a = (const uint8_t*)a->data;
+    g.sa = (const float*)a->scale;
+    g.b = (const uint8_t*)b->data;
+    g.sb = (const float*)b->scale;
+    g.c = out;
+    g.ws = (float*)ws;
+    return hip_status(launch_gemm(g, st));
+}
+
+// Checks the cache's and the batch's own fields (no pointer is read) and
+// fills kv. Pointers are checked by the callers that use them.
+static fq_status kv_args(const fq_kv_cache* c, const fq_kv_batch* b, KvArgs& kv)
+{
+    if (!c || !b)
+        return FQ_E_INVALID;
+    if (c->format < FQ_E4M3 || c->format > FQ_E2M1 || c->kv_heads < 1 || c->num_pages < 0)
+        return FQ_E_INVALID;
+    if (b->batch < 0 || b->max_pages < 0 || b->max_q < 0 || b->max_len < 0 || b->total_q < 0)
+        return FQ_E_INVALID;
+    if (c->format == FQ_E2M1 || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
+        return FQ_E_UNSUPPORTED;
+    auto pow2 = [](int32_t v, int32_t lo, int32_t hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; };
+    if (!pow2(c->page_tokens, 16, 256) || !pow2(c->block_tokens, 16, 128) || c->block_tokens > c->page_tokens)
+        return FQ_E_UNSUPPORTED;
+    const int64_t page = (int64_t)c->kv_heads * c->page_tokens * c->head_dim;
+    if (c->kv_heads > 4096 || c->num_pages > kMaxElems / page || c->num_pages > 0x7fffffff)
+        return FQ_E_SHAPE;
+    if (b->batch > 65535 || (int64_t)b->max_pages * c->page_tokens > (int64_t(1) << 30) || b->max_q > (1 << 24) ||
+        b->total_q > kMaxElems / ((int64_t)c->kv_heads * c->head_dim))
+        return FQ_E_SHAPE;
+    kv.fmt = c->format;
+    kv.heads = c->kv_heads;
+    kv.dim = c->head_dim;
+    kv.page = c->page_tokens;
+    kv.block = c->block_tokens;
+    kv.num_pages = c->num_pages;
+    kv.k = (uint8_t*)c->k;
+    kv.v = (uint8_t*)c->v;
+    kv.ks = c->k_scale;
+    kv.vs = c->v_scale;
+    kv.batch = b->batch;
+    kv.max_pages = b->max_pages;
+    kv.max_q = b->max_q;
+    const int64_t cap = (int64_t)b->max_pages * c->page_tokens;
+    kv.max_len = c->num_pages == 0 ? 0 : (int)(b->max_len == 0 || b->max_len > cap ? cap : b->max_len);
+    kv.total_q = b->total_q;
+    kv.table = b->page_table;
+    kv.lens = b->seq_lens;
+    kv.q_start = b->q_start;
+    return FQ_OK;
+}
+
+static fq_status check_kv_pointers(const KvArgs& kv)
+{
+    if (!kv.lens || (kv.max_len > 0 && (!kv.k || !kv.v || !kv.ks || !kv.vs || !kv.table)))
+        return FQ_E_INVALID;
+    if (!aligned(kv.k, 16) || !aligned(kv.v, 16) || !aligned(kv.ks, 16) || !aligned(kv.vs, 16) ||
+        !aligned(kv.table, 4) || !aligned(kv.lens, 4) || !aligned(kv.q_start, 4))
+        return FQ_E_ALIGN;
+    return FQ_OK;
+}
+
+fq_status fq_kv_append(const fq_kv_cache* c, const fq_kv_batch* b, int32_t in_dtype, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, hipStream_t st)
+{
+    KvArgs kv;
+    fq_status s = kv_args(c, b, kv);
+    if (s != FQ_OK)
+        return s;
+    if (in_dtype != FQ_IN_F32 && in_dtype != FQ_IN_BF16)
+        return FQ_E_INVALID;
+    const int64_t row = (int64_t)kv.heads * kv.dim;
+    if (k_stride < row || v_stride < row)
+        return FQ_E_INVALID;
+    if ((int64_t)kv.batch * ((kv.max_q + kv.block - 2) / kv.block + 1) > 0x7fffffff)
+        return FQ_E_SHAPE;
+    if (kv.batch == 0 || kv.max_q == 0 || kv.total_q == 0 || kv.max_len == 0)
+        return FQ_OK;
+    if (k_stride > kMaxElems / kv.total_q || v_stride > kMaxElems / kv.total_q)
+        return FQ_E_SHAPE;
+    if ((s = check_kv_pointers(kv)) != FQ_OK)
+        return s;
+    if (!k || !v)
+        return FQ_E_INVALID;
+    const int unit = in_dtype == FQ_IN_BF16 ? 8 : 4;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % unit || v_stride % unit)
+        return FQ_E_ALIGN;
+    return hip_status(launch_kv_append(kv, in_dtype == FQ_IN_BF16, k, k_stride, v, v_stride, st));
+}
+
+static fq_status attention_args(const fq_kv_cache* c, const fq_kv_batch* b, const fq_attention_desc* d, AttnArgs& a)
+{
+    const fq_status s = kv_args(c, b, a.kv);
+    if (s != FQ_OK)
+        return s;
+    // comparisons that a NaN fails
+    if (!d || d->q_heads < 1 || d->window < 0 || d->q_stride < 0 || !(d->scale - d->scale == 0.0f) ||
+        !(d->softcap >= 0.0f) || !(d->softcap - d->softcap == 0.0f))
+        return FQ_E_INVALID;
+    if (d->q_heads % a.kv.heads)
+        return FQ_E_UNSUPPORTED;
+    const int64_t row = (int64_t)d->q_heads * a.kv.dim;
+    a.q_stride = d->q_stride ? d->q_stride : row;
+    if (a.q_stride < row)
+        return FQ_E_INVALID;
+    if (d->q_heads > 65536 || (a.kv.total_q > 0 && a.q_stride > kMaxElems / a.kv.total_q) ||
+        (int64_t)a.kv.max_q * d->q_heads > (int64_t(1) << 30))
+        return FQ_E_SHAPE;
+    a.q_heads = d->q_heads;
+    a.window = d->window >= a.kv.max_len ? 0 : d->window;  // a window as long as any sequence hides nothing
+    a.scale = d->scale != 0.0f ? d->scale : a.kv.dim == 64 ? 0.125f : a.kv.dim == 128 ? 0.08838834764831845f : 0.0625f;
+    a.softcap = d->softcap;
+    return FQ_OK;
+}
+
+fq_status fq_attention_workspace(const fq_kv_cache* c, const fq_kv_batch* b, const fq_attention_desc* d, size_t* bytes)
+{
+    AttnArgs a;
+    const fq_status s = attention_args(c, b, d, a);
+    if (s != FQ_OK)
+        return s;
+    if (bytes)
+        *bytes = a.kv.batch == 0 || a.kv.max_q == 0 || a.kv.total_q == 0 ? 0 : plan_attention(a);
+    return FQ_OK;
+}
+
+fq_status fq_attention(const fq_kv_cache* c, const fq_kv_batch* b, const fq_attention_desc* d, const void* q, void* out,
+                       float* lse, void* ws, size_t ws_bytes, hipStream_t st)
+{
+    AttnArgs a;
+    fq_status s = attention_args(c, b, d, a);
+    if (s != FQ_OK)
+        return s;
+    if (a.kv.batch == 0 || a.kv.max_q == 0 || a.kv.total_q == 0)
+        return FQ_OK;
+    if ((s = check_kv_pointers(a.kv)) != FQ_OK)
+        return s;
+    if (!q || !out)
+        return FQ_E_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || a.q_stride % 8)
+        return FQ_E_ALIGN;
+    const size_t need = plan_attention(a);
+    if (need) {
+        if (!ws || ws_bytes < need)
+            return FQ_E_WORKSPACE;
+        if (!aligned(ws, 16))
+            return FQ_E_ALIGN;
+    }
+    a.q = (const uint16_t*)q;
+    a.out = (uint16_t*)out;
+    a.lse = lse;
+    a.ws = (float*)ws;
+    return hip_status(launch_attention(a, st));
+}
+
 }  // extern "C"

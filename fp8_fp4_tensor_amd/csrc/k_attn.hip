@@ -1,0 +1,383 @@
+// k_attn.hip -- attention over the paged 8-bit cache on gfx950.
+//
+//   s = scale * ks[block of t] * (q . K_t)      (then cap * tanh(s / cap))
+//   o = sum_t p_t * vs[block of t] * V_t,  p = softmax of s over the visible t
+//
+// The codes become bf16 in registers (exact: both 8-bit formats are subsets
+// of bf16) and meet bf16 queries in v_mfma_f32_16x16x32_bf16; the block
+// scales multiply scores and probabilities in fp32. p * vs is rounded to bf16
+// for the second product, at most 2^-8 of each term, as the bf16 output's own
+// rounding is of their sum; the sum of the unrounded p, the maxima and the
+// accumulators are fp32.
+//
+// Layout: no operand crosses lanes. The first product computes S^T = K Q^T,
+// K's tokens as the instruction's rows. A step takes 64 tokens as four row
+// tiles; row r of tile n is token 16 (r / 4) + 4 n + r % 4, so that the four
+// results a lane gets from each tile are, over the four tiles, 16
+// consecutive tokens of one query row. Those are just what the second
+// product O^T = V^T P^T wants from that lane as its column operand, and with
+// V stored transposed (a head's page is [dim, page_tokens]) the same 16
+// tokens of a value row are one 16-byte load. So a lane sees one block scale,
+// one page and one query row a step; the row statistics are per-lane scalars,
+// joined over the four lane groups by two exchanges.
+#include "codec.hpp"
+#include "launch.hpp"
+
+namespace fq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStep = 64;   // tokens a wave takes at once
+constexpr int kRows = 16;   // query rows of a workgroup
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+
+// Eight codes -> eight bf16 (exact).
+template <int FMT>
+__device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b)
+{
+    bf16x2 r[4];
+    if constexpr (FMT == kE4M3) {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    } else {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(a, 1.0f, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(a, 1.0f, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(b, 1.0f, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(b, 1.0f, true);
+    }
+    return bf16x8{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 rows, bf16x8 cols, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, cols, c, 0, 0, 0);
+}
+
+// cap * tanh(x / cap), by exp: 1 - 2 / (e^{2y} + 1).
+__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
+{
+    const float e = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
+    return cap * (1.0f - 2.0f / (e + 1.0f));
+}
+
+// The keys that the rows [r0, r1) of a sequence and head see: [lo, hi), empty
+// if hi <= lo; from is lo rounded down to a step.
+struct Span {
+    int lo, hi, from;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const KvSeq& s, int r0, int r1, int group)
+{
+    Span p;
+    const int first = s.len - s.nq;
+    const int pos0 = first + r0 / group, pos1 = first + (r1 - 1) / group;  // r1 > r0
+    p.hi = max(pos1 + 1, 0);
+    p.lo = a.window > 0 ? max(pos0 - a.window + 1, 0) : 0;
+    p.from = p.lo & ~(kStep - 1);
+    return p;
+}
+
+template <int D, int FMT, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
+{
+    constexpr int C = D / 64;  // 16-byte chunks of a key row a lane holds
+    constexpr int T = D / 16;  // value row tiles
+    __shared__ float lds_o[kWaves][kRows][D + 4];
+    __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int row = lane & 15, grp = lane >> 4;
+    const int group = a.q_heads / kv.heads;
+    // heads run fastest: workgroups go round robin to the XCDs, so with eight
+    // heads each XCD's L2 sees the keys and values of one of them
+    const unsigned ht = blockIdx.x / (unsigned)kv.heads;
+    const int h = (int)(blockIdx.x - ht * (unsigned)kv.heads);
+    const int r0 = (int)(ht % (unsigned)a.tiles) * kRows;
+    const int split = (int)(ht / (unsigned)a.tiles);
+    const int seq = (int)blockIdx.y;
+    const KvSeq s = kv_seq(kv, seq);
+    const int rows = s.nq * group;
+    if (r0 >= rows)
+        return;
+    const Span sp = span_of(a, s, r0, min(r0 + kRows, rows), group);
+    const int begin = sp.from + split * a.chunk;
+    const int end = SPLIT ? min(sp.hi, begin + a.chunk) : sp.hi;
+    if (SPLIT && begin >= end)
+        return;
+
+    const int r = min(r0 + row, rows - 1);  // rows past the last repeat it and are not stored
+    const int tok = r / group, head = h * group + r % group;
+    const int pos = s.len - s.nq + tok;
+    const int oldest = a.window > 0 ? pos - a.window + 1 : -0x7fffffff;
+    bf16x8 q[C][2];
+    {
+        const uint16_t* p = a.q + (s.q0 + tok) * a.q_stride + (int64_t)head * D + grp * 16;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            q[c][0] = __builtin_bit_cast(bf16x8, ld16(p + c * 64));
+            q[c][1] = __builtin_bit_cast(bf16x8, ld16(p + c * 64 + 8));
+        }
+    }
+    const float sc2 = a.scale * kLog2e;
+    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+    const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
+    const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block);
+
+    float m = -kInf, l = 0.0f;
+    f32x4 o[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int t0 = begin + w * kStep; t0 < end; t0 += kWaves * kStep) {
+        // the page of the tokens whose keys this lane loads, and of those it scores
+        const int tk = t0 + (row >> 2) * 16, tv = t0 + grp * 16;
+        int pk = table[min(tk >> ps, kv.max_pages - 1)], pv = table[min(tv >> ps, kv.max_pages - 1)];
+        const bool ok_k = pk >= 0 && pk < kv.num_pages, ok_v = pv >= 0 && pv < kv.num_pages;
+        pk = ok_k ? pk : 0;
+        pv = ok_v ? pv : 0;
+        const uint8_t* kp =
+            kv.k + (((int64_t)pk * kv.heads + h) * kv.page + (tk & (kv.page - 1)) + (row & 3)) * D + grp * 16;
+        const int64_t vt = ((int64_t)pv * kv.heads + h) * kv.page;
+        const uint8_t* vp = kv.v + vt * D + (int64_t)row * kv.page + (tv & (kv.page - 1));
+        const int64_t blk = (vt >> bs) + ((tv & (kv.page - 1)) >> bs);
+        const float ks = kv.ks[blk];
+        float vs = kv.vs[blk];
+        u32x4 kc[4][C], vc[T];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                kc[n][c] = ld16(kp + n * 4 * D + c * 64);
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            vc[t] = ld16(vp + (int64_t)t * 16 * kv.page);
+
+        float x[16];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                d = mfma(widen8<FMT>(kc[n][c][0], kc[n][c][1]), q[c][0], d);
+                d = mfma(widen8<FMT>(kc[n][c][2], kc[n][c][3]), q[c][1], d);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[n * 4 + e] = d[e];
+        }
+        if (a.softcap > 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[e] = soft_cap(x[e] * ks * a.scale, a.softcap, inv_cap) * kLog2e;
+        } else {
+            const float f = ks * sc2;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[e] *= f;
+        }
+        const bool inside = t0 >= sp.lo && t0 + kStep <= end && ok_v && t0 + kStep - 1 <= pos && t0 >= oldest;
+        if (!__all(inside)) {
+            // scores of keys that a row does not see go to -inf; values of keys
+            // that no row sees (a page's unused or outdated part) to zero, for
+            // they may hold anything and 0 * NaN is not 0
+            const int from = max(sp.lo - tv, 0), to = ok_v ? min(end - tv, 16) : 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const bool see = e >= from && e < to && tv + e <= pos && tv + e >= oldest;
+                x[e] = see ? x[e] : -kInf;
+            }
+            vs = from < to ? vs : 0.0f;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    keep |= (d * 4 + b >= from && d * 4 + b < to) ? 0xffu << (8 * b) : 0u;
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    vc[t][d] &= keep;
+            }
+        }
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e)
+            top = fmaxf(top, x[e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float mu = mn == -kInf ? 0.0f : mn;  // a row that has seen nothing yet
+        const float alpha = __builtin_amdgcn_exp2f(m - mu);
+        m = mn;
+        float sum = 0.0f;
+        bf16x8 p[2];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float v = __builtin_amdgcn_exp2f(x[e] - mu);
+            sum += v;
+            p[e >> 3][e & 7] = (__bf16)(v * vs);
+        }
+        l = l * alpha + sum;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            o[t] *= alpha;
+            o[t] = mfma(widen8<FMT>(vc[t][0], vc[t][1]), p[0], o[t]);
+            o[t] = mfma(widen8<FMT>(vc[t][2], vc[t][3]), p[1], o[t]);
+        }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (grp == 0) {
+        lds_m[w][row] = m;
+        lds_l[w][row] = l;
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        *(f32x4*)&lds_o[w][row][t * 16 + grp * 4] = o[t];
+    __syncthreads();
+    // thread -> row threadIdx / 16, dims (threadIdx % 16) * 4 + 64 i
+    const int orow = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
+    if (r0 + orow >= rows)
+        return;
+    float top = lds_m[0][orow];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i)
+        top = fmaxf(top, lds_m[i][orow]);
+    const float mu = top == -kInf ? 0.0f : top;
+    float f[kWaves], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        f[i] = __builtin_amdgcn_exp2f(lds_m[i][orow] - mu);
+        sum += lds_l[i][orow] * f[i];
+    }
+    const int ro = r0 + orow;
+    const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    if (!SPLIT && a.lse && d0 == 0)
+        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
+    if (SPLIT && d0 == 0)
+        *(float2*)(a.ws + (rid * a.splits + split) * 2) = make_float2(top, sum);
+    float* part = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + (rid * a.splits + split) * D;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const int d = d0 + c * 64;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i)
+            v += *(const f32x4*)&lds_o[i][orow][d] * f[i];
+        if constexpr (SPLIT) {
+            *(f32x4*)(part + d) = v;
+        } else {
+            uint16_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
+            *(u32x2*)(a.out + rid * D + d) = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+        }
+    }
+}
+
+// Joins the partial results of a row's splits, in their order.
+template <int D>
+__global__ __launch_bounds__(D / 4) void k_attn_join(AttnArgs a)
+{
+    const KvArgs& kv = a.kv;
+    const int group = a.q_heads / kv.heads;
+    const KvSeq s = kv_seq(kv, (int)blockIdx.y);
+    const unsigned at = blockIdx.x / (unsigned)kv.heads;
+    const int ro = (int)at, h = (int)(blockIdx.x - at * (unsigned)kv.heads), rows = s.nq * group;
+    if (ro >= rows)
+        return;
+    const int r0 = ro / kRows * kRows;
+    const Span sp = span_of(a, s, r0, min(r0 + kRows, rows), group);
+    const int n = sp.hi > sp.from ? (int)cdiv(sp.hi - sp.from, a.chunk) : 0;
+    const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
+    const float2* ml = (const float2*)a.ws + rid * a.splits;
+    const float* part = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + rid * a.splits * D + threadIdx.x * 4;
+    float top = -kInf;
+    for (int i = 0; i < n; ++i)
+        top = fmaxf(top, ml[i].x);
+    const float mu = top == -kInf ? 0.0f : top;
+    float sum = 0.0f;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - mu);
+        sum += ml[i].y * f;
+        v += *(const f32x4*)(part + (int64_t)i * D) * f;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint16_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
+    *(u32x2*)(a.out + rid * D + threadIdx.x * 4) = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+    if (a.lse && threadIdx.x == 0)
+        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
+}
+
+template <int D, int FMT>
+hipError_t run(const AttnArgs& a, hipStream_t st)
+{
+    const dim3 grid((unsigned)((int64_t)a.splits * a.tiles * a.kv.heads), (unsigned)a.kv.batch);
+    if (a.splits == 1) {
+        k_attn<D, FMT, false><<<grid, kWaves * 64, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    k_attn<D, FMT, true><<<grid, kWaves * 64, 0, st>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    const dim3 jgrid((unsigned)((int64_t)a.kv.max_q * a.q_heads), (unsigned)a.kv.batch);
+    k_attn_join<D><<<jgrid, D / 4, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t by_format(const AttnArgs& a, hipStream_t st)
+{
+    return a.kv.fmt == kE4M3 ? run<D, kE4M3>(a, st) : run<D, kE5M2>(a, st);
+}
+
+}  // namespace
+
+size_t plan_attention(AttnArgs& a)
+{
+    const KvArgs& kv = a.kv;
+    const int64_t group = a.q_heads / kv.heads;
+    a.tiles = (int)cdiv(kv.max_q * group, kRows);
+    const int64_t tiles = (int64_t)kv.batch * kv.heads * a.tiles;
+    int64_t span = kv.max_len;
+    if (a.window > 0 && span > (int64_t)a.window + kv.max_q + kStep)
+        span = (int64_t)a.window + kv.max_q + kStep;
+    // one workgroup per tile if the tiles alone fill the chip; else about 1024
+    // workgroups, each with at least a step for each of its waves
+    const int64_t least = kWaves * kStep;
+    int64_t splits = tiles >= 512 ? 1 : cdiv(1024, tiles > 0 ? tiles : 1);
+    int64_t chunk = cdiv(cdiv(span, splits), least) * least;
+    if (chunk < least)
+        chunk = least;
+    splits = cdiv(span, chunk);
+    a.chunk = (int)chunk;
+    a.splits = (int)(splits < 1 ? 1 : splits);
+    if (a.splits == 1)
+        return 0;
+    return (size_t)(kv.total_q * a.q_heads) * a.splits * (kv.dim + 2) * sizeof(float);
+}
+
+hipError_t launch_attention(const AttnArgs& a, hipStream_t st)
+{
+    switch (a.kv.dim) {
+    case 64: return by_format<64>(a, st);
+    case 128: return by_format<128>(a, st);
+    default: return by_format<256>(a, st);
+    }
+}
+
+}  // namespace fq

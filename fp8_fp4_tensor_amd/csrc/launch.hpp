@@ -189,4 +189,78 @@ hipError_t launch_dequant_mx(const uint8_t* q, const uint8_t* e, int fmt, int64_
 hipError_t launch_dequant_nvfp4(const uint8_t* p, const uint8_t* codes, const float* S, int64_t R, int64_t C,
                                 int br, int bc, void* y, int bf, hipStream_t stream);
 
+// The product of blockwise-scaled E4M3 planes, C = A B^T (k_gemm.hip).
+struct GemmArgs {
+    int64_t m = 0, n = 0, k = 0;     // m, n >= 1; k a multiple of 128
+    const uint8_t* a = nullptr;      // [m, k] codes
+    const float* sa = nullptr;       // [m, k/128]
+    const uint8_t* b = nullptr;      // [n, k] codes
+    const float* sb = nullptr;       // [n, k/128] if b1, else [n/128, k/128]
+    void* c = nullptr;               // [m, n] fp32, or bf16 if bf
+    int b1 = 0, bf = 0, acc = 0;     // acc: C += (fp32 only)
+    int pow2 = 0;                    // every scale is a power of two of at least 2^-127
+    float* ws = nullptr;
+};
+// Workspace bytes of a product of this shape (m, n, k, b1 and bf set).
+size_t gemm_workspace(const GemmArgs& g);
+hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream);
+
+// One 8-bit key/value cache and the sequences a call touches (k_kv.hip, k_attn.hip).
+struct KvArgs {
+    int fmt = 0, heads = 0, dim = 0, page = 0, block = 0;  // page, block: powers of two, block <= page
+    int64_t num_pages = 0;
+    uint8_t* k = nullptr;            // [num_pages, heads, page, dim]
+    uint8_t* v = nullptr;            // [num_pages, heads, dim, page]
+    float* ks = nullptr;             // [num_pages, heads, page/block]
+    float* vs = nullptr;
+    int batch = 0, max_pages = 0, max_q = 0, max_len = 0;
+    int64_t total_q = 0;
+    const int32_t* table = nullptr;  // [batch, max_pages]
+    const int32_t* lens = nullptr;   // [batch]
+    const int32_t* q_start = nullptr;  // [batch + 1]
+};
+
+// Sequence b of a call: its tokens in the cache and its rows of this call,
+// held to what the tables can hold whatever the device values are.
+struct KvSeq {
+    int len, nq;
+    int64_t q0;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& kv, int b)
+{
+    KvSeq s;
+    const int64_t cap = (int64_t)kv.max_pages * kv.page;
+    const int64_t most = kv.max_len < cap ? kv.max_len : cap;
+    const int64_t len = kv.lens[b];
+    s.len = (int)(len < 0 ? 0 : len > most ? most : len);
+    int64_t q0 = kv.q_start ? (int64_t)kv.q_start[b] : (int64_t)b * kv.max_q;
+    int64_t q1 = kv.q_start ? (int64_t)kv.q_start[b + 1] : q0 + kv.max_q;
+    q0 = q0 < 0 ? 0 : q0 > kv.total_q ? kv.total_q : q0;
+    q1 = q1 < q0 ? q0 : q1 > kv.total_q ? kv.total_q : q1;
+    s.q0 = q0;
+    s.nq = (int)(q1 - q0 > kv.max_q ? kv.max_q : q1 - q0);
+    return s;
+}
+
+// Quantize new keys and values ([total_q, heads, dim], token strides in
+// elements) into the last positions of their sequences.
+hipError_t launch_kv_append(const KvArgs& kv, int in_bf16, const void* k_new, int64_t k_stride, const void* v_new,
+                            int64_t v_stride, hipStream_t stream);
+
+struct AttnArgs {
+    KvArgs kv;
+    int q_heads = 0, window = 0;
+    float scale = 0.0f, softcap = 0.0f;
+    const uint16_t* q = nullptr;     // [total_q, q_heads, dim] bf16, token stride q_stride
+    int64_t q_stride = 0;
+    uint16_t* out = nullptr;         // [total_q, q_heads, dim] bf16
+    float* lse = nullptr;            // [total_q, q_heads] or null
+    float* ws = nullptr;             // partial results of split sequences
+    int tiles = 0;                   // row tiles of the longest run of queries
+    int chunk = 0, splits = 1;       // tokens a split, splits of the longest sequence
+};
+// Sets tiles, chunk and splits of a call from its shape alone; returns the workspace bytes.
+size_t plan_attention(AttnArgs& a);
+hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
+
 }  // namespace fq

@@ -54,6 +54,29 @@ class FqDelayedState(ctypes.Structure):
                 ("scale_inv", ctypes.c_void_p), ("pending", ctypes.c_void_p), ("step", ctypes.c_int64)]
 
 
+class FqGemmDesc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("b_block_rows", ctypes.c_int32),
+                ("scale_mode", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class FqKvCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("block_tokens", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class FqKvBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("total_q", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+
+
+class FqAttentionDesc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("q_stride", ctypes.c_int64)]
+
+
 class FqError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -75,6 +98,11 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     dp = ctypes.POINTER(FqDesc)
     qp = ctypes.POINTER(FqQuantized)
+    pp = ctypes.POINTER(FqPlane)
+    gp = ctypes.POINTER(FqGemmDesc)
+    cp = ctypes.POINTER(FqKvCache)
+    bp = ctypes.POINTER(FqKvBatch)
+    ap = ctypes.POINTER(FqAttentionDesc)
     sig = {
         "fq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "fq_sizes": (ctypes.c_int, [dp, _SZ, _SZ, _SZ, _SZ, _SZ]),
@@ -86,6 +114,11 @@ def lib():
         "fq_dequantize": (ctypes.c_int, [dp, qp, ctypes.c_int32, _P, ctypes.c_int32, _P]),
         "fq_requantize_transpose": (ctypes.c_int, [dp, qp, qp, _P]),
         "fq_quantize_noalloc": (ctypes.c_int, [dp, _P, qp, _P]),
+        "fq_gemm_workspace": (ctypes.c_int, [gp, _SZ]),
+        "fq_gemm": (ctypes.c_int, [gp, pp, pp, _P, _P, ctypes.c_size_t, _P]),
+        "fq_kv_append": (ctypes.c_int, [cp, bp, ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
+        "fq_attention_workspace": (ctypes.c_int, [cp, bp, ap, _SZ]),
+        "fq_attention": (ctypes.c_int, [cp, bp, ap, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -283,3 +316,163 @@ def fq_requantize_transpose(d: FqDesc, src: Quantized, dst: Quantized, stream=No
     a, b = src.c(), dst.c()
     _check(lib().fq_requantize_transpose(ctypes.byref(d), ctypes.byref(a), ctypes.byref(b), _stream(stream)),
            "fq_requantize_transpose")
+
+
+# ---------------------------------------------------------------- operators on 8-bit data
+class Plane:
+    """One quantized copy as an operand: codes and scales (kept alive here)."""
+
+    def __init__(self, data: torch.Tensor, scale: torch.Tensor):
+        if not (data.is_contiguous() and scale.is_contiguous()):
+            raise ValueError("planes are contiguous")
+        if data.element_size() != 1 or scale.dtype != torch.float32:
+            raise TypeError("blockwise planes are 8-bit codes and float32 scales")
+        self.data, self.scale = data, scale
+        self._c = FqPlane(data.data_ptr(), scale.data_ptr())
+
+    @classmethod
+    def rowwise(cls, q: Quantized) -> "Plane":
+        return cls(q.row_data, q.row_scale)
+
+    @classmethod
+    def colwise(cls, q: Quantized) -> "Plane":
+        return cls(q.col_data, q.col_scale)
+
+
+def gemm_desc(m: int, n: int, k: int, b_block_rows: int = 128, out_dtype: int = FQ_IN_BF16,
+              scale_mode: int = FQ_SCALE_DEFAULT, accumulate: bool = False) -> FqGemmDesc:
+    return FqGemmDesc(m, n, k, b_block_rows, scale_mode, out_dtype, int(accumulate))
+
+
+def fq_gemm_workspace(d: FqGemmDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().fq_gemm_workspace(ctypes.byref(d), ctypes.byref(n)), "fq_gemm_workspace")
+    return n.value
+
+
+def alloc_gemm_workspace(d: FqGemmDesc, device="cuda") -> Optional[torch.Tensor]:
+    n = fq_gemm_workspace(d)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _nbytes(ws: Optional[torch.Tensor]) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def fq_gemm(d: FqGemmDesc, a: Plane, b: Plane, out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
+    """out [m, n] = A B^T of two blockwise planes (out += with d.accumulate)."""
+    if a.data.numel() != d.m * d.k or b.data.numel() != d.n * d.k or out.numel() != d.m * d.n:
+        raise ValueError("a is [m, k], b is [n, k] and out is [m, n]")
+    nb = d.k // 128
+    if a.scale.numel() != d.m * nb or b.scale.numel() != (d.n if d.b_block_rows == 1 else d.n // 128) * nb:
+        raise ValueError("a scale for each block of 128 (and for 128 rows of b with b_block_rows 128)")
+    if in_dtype_of(out) != d.out_dtype or not out.is_contiguous():
+        raise TypeError("out is contiguous and of the descriptor's out_dtype")
+    _check(lib().fq_gemm(ctypes.byref(d), ctypes.byref(a._c), ctypes.byref(b._c), out.data_ptr(),
+                         None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_gemm")
+
+
+class KvCache:
+    """A paged 8-bit key/value cache (buffers and their shape)."""
+
+    def __init__(self, fmt: int, block_tokens: int, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        pages, heads, page, dim = k.shape
+        if tuple(v.shape) != (pages, heads, dim, page):
+            raise ValueError("k is [pages, heads, page_tokens, dim] and v is [pages, heads, dim, page_tokens]")
+        if block_tokens < 1 or any(tuple(s.shape) != (pages, heads, page // block_tokens) for s in (k_scale, v_scale)):
+            raise ValueError("scales are [pages, heads, page_tokens / block_tokens]")
+        if any(t.element_size() != 1 for t in (k, v)) or any(s.dtype != torch.float32 for s in (k_scale, v_scale)):
+            raise TypeError("codes are 8-bit and scales float32")
+        if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
+            raise ValueError("cache buffers are contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.fmt, self.block_tokens = fmt, block_tokens
+        self.heads, self.dim, self.page_tokens, self.pages = heads, dim, page, pages
+        self._c = FqKvCache(fmt, heads, dim, page, block_tokens, pages, k.data_ptr(), v.data_ptr(),
+                            k_scale.data_ptr(), v_scale.data_ptr())
+
+
+def alloc_kv_cache(fmt: int, pages: int, heads: int, dim: int, page_tokens: int = 64, block_tokens: int = 64,
+                   device="cuda") -> KvCache:
+    """An empty cache; its contents need no initialization."""
+    if block_tokens < 1 or page_tokens % block_tokens:
+        raise ValueError("a page holds whole blocks")
+    s = (pages, heads, page_tokens // block_tokens)
+    return KvCache(fmt, block_tokens,
+                   torch.empty((pages, heads, page_tokens, dim), dtype=torch.uint8, device=device),
+                   torch.empty((pages, heads, dim, page_tokens), dtype=torch.uint8, device=device),
+                   torch.empty(s, dtype=torch.float32, device=device),
+                   torch.empty(s, dtype=torch.float32, device=device))
+
+
+class KvBatch:
+    """The sequences of a call: page_table [batch, max_pages], seq_lens [batch]
+    and q_start [batch + 1] are int32 device tensors (q_start None: max_q rows
+    of every sequence); max_len bounds seq_lens (0: what the table holds)."""
+
+    def __init__(self, page_table: torch.Tensor, seq_lens: torch.Tensor, q_start: Optional[torch.Tensor],
+                 total_q: int, max_q: int, max_len: int = 0):
+        given = [t for t in (page_table, seq_lens, q_start) if t is not None]
+        if any(t.dtype != torch.int32 or not t.is_contiguous() for t in given):
+            raise TypeError("page_table, seq_lens and q_start are contiguous int32")
+        batch, max_pages = page_table.shape
+        if seq_lens.numel() != batch or (q_start is not None and q_start.numel() != batch + 1):
+            raise ValueError("seq_lens has batch entries and q_start batch + 1")
+        self.page_table, self.seq_lens, self.q_start = page_table, seq_lens, q_start
+        self.total_q, self.max_q, self.max_len = total_q, max_q, max_len
+        self._c = FqKvBatch(batch, max_pages, max_q, max_len, total_q, page_table.data_ptr(), seq_lens.data_ptr(),
+                            None if q_start is None else q_start.data_ptr())
+
+
+def _rows3(t: torch.Tensor, total: int, heads: int, dim: int, what: str) -> int:
+    """The token stride of a [total, heads, dim] tensor whose tokens are each contiguous."""
+    if tuple(t.shape) != (total, heads, dim):
+        raise ValueError(f"{what} is [total_q, heads, head_dim]")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{what}: a token's heads are contiguous")
+    return t.stride(0) if total > 1 else heads * dim
+
+
+def fq_kv_append(cache: KvCache, batch: KvBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
+    """Quantize k_new and v_new [total_q, heads, dim] into the last positions of their sequences."""
+    ks = _rows3(k_new, batch.total_q, cache.heads, cache.dim, "k_new")
+    vs = _rows3(v_new, batch.total_q, cache.heads, cache.dim, "v_new")
+    dt = in_dtype_of(k_new)
+    if v_new.dtype != k_new.dtype:
+        raise TypeError("k_new and v_new have one dtype")
+    _check(lib().fq_kv_append(ctypes.byref(cache._c), ctypes.byref(batch._c), dt, k_new.data_ptr(), ks,
+                              v_new.data_ptr(), vs, _stream(stream)), "fq_kv_append")
+
+
+def attention_desc(q_heads: int, scale: float = 0.0, window: int = 0, softcap: float = 0.0) -> FqAttentionDesc:
+    return FqAttentionDesc(q_heads, window, scale, softcap, 0)
+
+
+def fq_attention_workspace(cache: KvCache, batch: KvBatch, d: FqAttentionDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().fq_attention_workspace(ctypes.byref(cache._c), ctypes.byref(batch._c), ctypes.byref(d),
+                                        ctypes.byref(n)), "fq_attention_workspace")
+    return n.value
+
+
+def alloc_attention_workspace(cache: KvCache, batch: KvBatch, d: FqAttentionDesc,
+                              device="cuda") -> Optional[torch.Tensor]:
+    n = fq_attention_workspace(cache, batch, d)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def fq_attention(cache: KvCache, batch: KvBatch, d: FqAttentionDesc, q: torch.Tensor, out: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """out [total_q, q_heads, dim] bf16 (and lse [total_q, q_heads] fp32) = attention of q over the cache."""
+    d.q_stride = _rows3(q, batch.total_q, d.q_heads, cache.dim, "q")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise TypeError("q and out are bfloat16")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out is contiguous and of q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != batch.total_q * d.q_heads
+                            or not lse.is_contiguous()):
+        raise TypeError("lse is contiguous float32 [total_q, q_heads]")
+    _check(lib().fq_attention(ctypes.byref(cache._c), ctypes.byref(batch._c), ctypes.byref(d), q.data_ptr(),
+                              out.data_ptr(), None if lse is None else lse.data_ptr(),
+                              None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_attention")

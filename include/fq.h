@@ -412,6 +412,164 @@ fq_status fq_requantize_transpose(const fq_desc *desc, const fq_quantized *in, c
  */
 fq_status fq_quantize_noalloc(const fq_desc *desc, const void *x, const fq_quantized *out, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators on 8-bit data
+ * ---------------------------------------------------------------------------
+ *
+ * The matrix product of two blockwise-scaled E4M3 planes,
+ *
+ *   C[i,j] = sum_b sa[i,b] * sb[j,b] * sum_{t<128} A[i, 128b+t] * B[j, 128b+t]
+ *
+ * A: [m, k] codes, scales [m, k/128] (1x128 tiles). B: [n, k] codes, scales
+ * [n/128, k/128] (128x128 tiles, b_block_rows = 128, n % 128 == 0) or
+ * [n, k/128] (1x128 tiles, b_block_rows = 1). Both are planes as FQ_BLOCK_FP32
+ * writes them, so the three products of a linear layer Y = X W^T are
+ *   forward  Y  [T,O]   a = X's rowwise plane,  b = W's rowwise plane (128x128)
+ *   dgrad    dX [T,I]   a = dY's rowwise plane, b = W's colwise plane (128x128)
+ *   wgrad    dW [O,I]   a = dY's colwise plane, b = X's colwise plane (1x128)
+ * Scaling and the sum over blocks are fp32; the result is rounded once to
+ * out_dtype. The inner sums are fp32 for fp32 outputs; for bf16 outputs they
+ * come from the 8-bit matrix instruction, which keeps each product to about
+ * 2^-12 of the largest of its block (1e-5 to 5e-5 of the result, against the
+ * output's rounding of 2^-8). Products sa * sb must be finite in fp32.
+ *   scale_mode   FQ_SCALE_POW2 declares that every scale of both planes is a
+ *                power of two (planes quantized with FQ_SCALE_POW2); the
+ *                result is the same sum, the scaling then exact.
+ *   accumulate   1: C += the product (FQ_IN_F32 only), 0: C = the product.
+ *   k % 128 == 0; m*k, n*k and m*n at most 2^36, k at most 2^23.
+ * k = 0 gives zeros (or leaves C with accumulate); m = 0 or n = 0 does nothing.
+ * The result does not depend on the run: no atomics, sums in a fixed order.
+ */
+typedef struct {
+    int64_t m, n, k;
+    int32_t b_block_rows; /* 1 or 128 */
+    int32_t scale_mode;   /* fq_scale_mode */
+    int32_t out_dtype;    /* fq_in_dtype of C */
+    int32_t accumulate;
+} fq_gemm_desc;
+
+/* Device scratch bytes of fq_gemm for this desc (0 for many shapes). */
+fq_status fq_gemm_workspace(const fq_gemm_desc *desc, size_t *workspace);
+
+/* C = A B^T as above; out is [m, n], row-major, 16-byte aligned. A NULL
+ * workspace is accepted where fq_gemm_workspace reports 0. */
+fq_status fq_gemm(const fq_gemm_desc *desc, const fq_plane *a, const fq_plane *b, void *out, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * A paged key/value cache in 8 bits, with one fp32 scale for each block of
+ * block_tokens tokens and head. A stored value is dec(code) * scale.
+ *   format        FQ_E4M3 or FQ_E5M2
+ *   head_dim      64, 128 or 256
+ *   page_tokens   tokens of a page: a power of two from 16 to 256
+ *   block_tokens  tokens of a scale: a power of two from 16 to 128, at most
+ *                 page_tokens
+ *   k             [num_pages, kv_heads, page_tokens, head_dim] codes
+ *   v             [num_pages, kv_heads, head_dim, page_tokens] codes
+ *                 (transposed: the second product of attention contracts over
+ *                 tokens, so tokens run along memory)
+ *   k_scale, v_scale  [num_pages, kv_heads, page_tokens / block_tokens]
+ * num_pages * kv_heads * page_tokens * head_dim <= 2^36. Nothing needs
+ * initialization: what a sequence has not written is never used.
+ */
+typedef struct {
+    int32_t format;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t block_tokens;
+    int64_t num_pages;
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+} fq_kv_cache;
+
+/*
+ * The sequences of one call. Token t of sequence i is slot t % page_tokens of
+ * page page_table[i, t / page_tokens]. The call's rows (new tokens, queries)
+ * of sequence i are rows q_start[i] .. q_start[i+1]-1 of its tensors, and are
+ * the last positions of the sequence: row j is position
+ * seq_lens[i] - (q_start[i+1] - q_start[i]) + j.
+ *   batch       sequences, 0 .. 65535
+ *   max_pages   columns of page_table; max_pages * page_tokens <= 2^30
+ *   max_q       the largest number of rows of one sequence
+ *   max_len     the largest seq_lens entry (0: max_pages * page_tokens); it
+ *               sets how the work is split
+ *   total_q     rows of the call's tensors
+ *   page_table  [batch, max_pages] device int32, only the entries below
+ *               ceil(seq_lens[i] / page_tokens) are used
+ *   seq_lens    [batch] device int32: tokens in the cache, this call's included
+ *   q_start     [batch + 1] device int32, ascending, or NULL for max_q rows
+ *               of every sequence
+ * The device values are read by the kernels, so the host cannot check them;
+ * the kernels hold every index to the declared sizes instead: lengths are cut
+ * to max_len and the table's span, rows to total_q and max_q, and the
+ * tokens of a page outside [0, num_pages) count as absent (not stored, not
+ * seen). A page must belong to one sequence of a call.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t max_pages;
+    int32_t max_q;
+    int32_t max_len;
+    int64_t total_q;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    const int32_t *q_start;
+} fq_kv_batch;
+
+/*
+ * Quantize new keys and values into the cache, at the last positions of their
+ * sequences. k_new and v_new: [total_q, kv_heads, head_dim] of in_dtype, a
+ * token's heads contiguous, tokens k_stride / v_stride elements apart (so a
+ * projection's joint output is taken as it is; pointers and strides 16-byte
+ * aligned). For each block of tokens and head, with a = max|x| over its new
+ * tokens, s = the smallest power of two of at least 2^-126 with a <= Fmax * s;
+ * if the block holds older tokens and their scale is larger, that one is
+ * kept, and if it is smaller their codes are moved to the new one,
+ * q' = Q(fp32(dec(q) * fp32(s_old / s))). New codes are Q(x / s), to nearest even.
+ * Powers of two make the move exact but for results in the format's
+ * subnormals. Rows at negative positions are skipped.
+ */
+fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32_t in_dtype, const void *k_new,
+                       int64_t k_stride, const void *v_new, int64_t v_stride, hipStream_t stream);
+
+/*
+ * Attention of the batch's rows over the cache:
+ *   s_t = scale * (q . K_t),   with softcap > 0: s_t = softcap * tanh(s_t / softcap)
+ *   p = softmax of s over the visible t,   out = sum_t p_t V_t
+ *   lse = log sum_t exp(s_t)   (natural logarithm)
+ * A row at position x sees the tokens t <= x, and with window > 0 only
+ * t > x - window. A row that sees nothing gets out = 0 and lse = -inf.
+ *   q_heads   a multiple of kv_heads; query head h reads kv head
+ *             h / (q_heads / kv_heads)
+ *   scale     0 selects 1 / sqrt(head_dim)
+ *   q         [total_q, q_heads, head_dim] bf16, tokens q_stride elements apart
+ *   out       [total_q, q_heads, head_dim] bf16, contiguous
+ *   lse       [total_q, q_heads] fp32, or NULL
+ * Cached tokens that a row of the call sees must have finite codes and
+ * scales; what no row of the call sees (a page's unused end, pages that
+ * a window has left behind) may hold anything. Scores, softmax and sums are
+ * fp32; probabilities are rounded to bf16 for the product with V.
+ */
+typedef struct {
+    int32_t q_heads;
+    int32_t window;
+    float scale;
+    float softcap;
+    int64_t q_stride; /* elements, 0: q_heads * head_dim */
+} fq_attention_desc;
+
+/* Device scratch bytes of fq_attention for this call (no pointer is read). */
+fq_status fq_attention_workspace(const fq_kv_cache *cache, const fq_kv_batch *batch, const fq_attention_desc *desc,
+                                 size_t *workspace);
+
+fq_status fq_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, const fq_attention_desc *desc,
+                       const void *q, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char *fq_status_str(fq_status status);
 
