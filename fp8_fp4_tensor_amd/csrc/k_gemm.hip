@@ -206,15 +206,206 @@ hipError_t few(const GemmArgs& g, hipStream_t st)
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- many rows
+// One workgroup computes a TM x TN tile of C, WM x WN waves of
+// (TM/WM) x (TN/WN). A step is one scale block: TM + TN rows of 128 bytes
+// come straight from memory into LDS (16 bytes a lane, no registers), one
+// step ahead of the products. The 16-byte chunk c of row r is kept at chunk
+// c ^ (r % 8) of its row, so that eight lanes reading one chunk of eight rows
+// meet no bank twice; the transfer writes LDS in lane order, so it is the
+// lane's source address that carries the permutation.
+
+// 64 lanes' 16 (or 4) bytes each -> LDS at `to`, in lane order. Written as
+// assembly because the compiler, which cannot tell the two stages apart,
+// would wait for every transfer before the next read of LDS; there is no
+// output register, and the waits are those of the step loop. M0 holds the
+// LDS address and needs one wait state before its use; nothing else here uses
+// it.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t to, int lane_offset, int offset)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                     :
+                     : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
+                     : "memory");
+}
+
+// Workgroup -> tile. Workgroups go to the eight XCDs round robin and each XCD
+// has its own L2, so an XCD takes a run of consecutive tiles; runs walk down
+// groups of eight tile rows, so the ~32 tiles an XCD works on at once share
+// their rows of A and of B.
+__device__ __forceinline__ void tile_of(const GemmArgs& g, int64_t& tm, int64_t& tn)
+{
+    const uint32_t total = gridDim.x, per = total / 8, rest = total % 8;
+    const uint32_t xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
+    const uint32_t t = xcd * per + min(xcd, rest) + nth;
+    const uint32_t wide = 8 * (uint32_t)g.tiles_n;
+    const uint32_t band = t / wide, in = t - band * wide;
+    const uint32_t high = min(8u, (uint32_t)g.tiles_m - band * 8);
+    tn = in / high;
+    tm = band * 8 + (in - (uint32_t)tn * high);
+}
+
+template <int TM, int TN, int WM, int WN, bool B1, bool BF>
+struct Tile {
+    static constexpr int kNW = WM * WN;
+    static constexpr int kMT = TM / WM / 16, kNT = TN / WN / 16;
+    static_assert(B1 || TN / WN <= 128, "a wave's columns share a 128x128 scale");
+    struct alignas(1024) Stage {
+        uint8_t a[TM * 128], b[TN * 128];
+        float sa[TM], sb[B1 ? TN : 64];
+    };
+};
+
+template <int TM, int TN, int WM, int WN, bool B1, bool BF>
+__global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
+{
+    using T = Tile<TM, TN, WM, WN, B1, BF>;
+    constexpr int NW = T::kNW, MT = T::kMT, NT = T::kNT;
+    constexpr int IA = TM / 8 / NW, IB = TN / 8 / NW;  // transfers of 8 rows a wave issues
+    static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole transfers");
+    __shared__ typename T::Stage stage[2];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 15, grp = lane >> 4;
+    int64_t tm, tn;
+    tile_of(g, tm, tn);
+    const int64_t m0 = tm * TM, n0 = tn * TN;
+    const int nb = (int)(g.k >> 7);
+    const int rows_a = (int)min((int64_t)TM, g.m - m0), rows_b = (int)min((int64_t)TN, g.n - n0);
+    const uint8_t* pa = g.a + m0 * g.k;
+    const uint8_t* pb = g.b + n0 * g.k;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)pa, 0, (int)(rows_a * g.k), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)pb, 0, (int)(rows_b * g.k), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rsa =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(g.sa + m0 * nb), 0, rows_a * nb * 4, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(g.sb + (B1 ? n0 : n0 >> 7) * nb), 0, (B1 ? rows_b : (rows_b + 127) >> 7) * nb * 4, 0x00020000);
+    // rows past the last repeat it, so every source address is inside; they are not stored
+    int va[IA], vb[IB], vsa, vsb;
+    const int sub = lane >> 3, chunk = (lane & 7) ^ sub;
+#pragma unroll
+    for (int i = 0; i < IA; ++i)
+        va[i] = min((w * IA + i) * 8 + sub, rows_a - 1) * (int)g.k + chunk * 16;
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+        vb[i] = min((w * IB + i) * 8 + sub, rows_b - 1) * (int)g.k + chunk * 16;
+    vsa = min(w * 64 + lane, rows_a - 1) * nb * 4;
+    vsb = min((w - TM / 64) * 64 + lane, (B1 ? rows_b : (rows_b + 127) >> 7) - 1) * nb * 4;
+
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)stage;
+    auto fill = [&](int which, int b) {
+        const uint32_t to = at + which * (uint32_t)sizeof(typename T::Stage);
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+            to_lds<16>(rb, to + offsetof(typename T::Stage, b) + (w * IB + i) * 1024, vb[i], b * 128);
+#pragma unroll
+        for (int i = 0; i < IA; ++i)
+            to_lds<16>(ra, to + (w * IA + i) * 1024, va[i], b * 128);
+        if (w < TM / 64)
+            to_lds<4>(rsa, to + offsetof(typename T::Stage, sa) + w * 256, vsa, b * 4);
+        else if (w < TM / 64 + (B1 ? TN / 64 : 1))
+            to_lds<4>(rsb, to + offsetof(typename T::Stage, sb) + (w - TM / 64) * 256, vsb, b * 4);
+    };
+    const int wm = w / WN, wn = w % WN;
+    const int c0 = ((grp ^ (row & 7)) * 16), c1 = c0 ^ 64;
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto work = [&](const typename T::Stage& s) {
+        i32x8 fa[MT];
+        float sc[MT];
+        const float sbv = s.sb[wn * (TN / WN) / 128];  // 128x128 tiles: one scale for the wave's columns
+        const uint8_t* qa = s.a + (wm * (TM / WM) + row) * 128;
+        const uint8_t* qb = s.b + (wn * (TN / WN) + row) * 128;
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+            fa[u] = join(ld16(qa + u * 2048 + c0), ld16(qa + u * 2048 + c1));
+            sc[u] = s.sa[wm * (TM / WM) + u * 16 + row];
+            if constexpr (!B1)
+                sc[u] *= sbv;
+        }
+        // the next column tile's operand is read during this one's products;
+        // the fences keep the scheduler from reading them all at once, which
+        // would not fit the registers
+        i32x8 fb = join(ld16(qb + c0), ld16(qb + c1));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            i32x8 next = fb;
+            if (t + 1 < NT)
+                next = join(ld16(qb + (t + 1) * 2048 + c0), ld16(qb + (t + 1) * 2048 + c1));
+            f32x4 sb4;
+            if constexpr (B1)
+                sb4 = *(const f32x4*)&s.sb[wn * (TN / WN) + t * 16 + grp * 4];
+#pragma unroll
+            for (int u = 0; u < MT; ++u) {
+                const f32x4 p = mfma_block<BF>(fb, fa[u]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[t][u][e] = __builtin_fmaf(p[e], B1 ? sc[u] * sb4[e] : sc[u], acc[t][u][e]);
+            }
+            fb = next;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // Each wave waits for its own transfers before the barrier; after it the
+    // step's stage is whole, and every wave has read the other one.
+    fill(0, 0);
+    for (int b = 0; b < nb; ++b) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (b + 1 < nb)
+            fill((b + 1) & 1, b + 1);
+        work(stage[b & 1]);
+    }
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+        const int64_t i = m0 + wm * (TM / WM) + u * 16 + row;
+        if (i < g.m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                store4<BF>(g.c, i, n0 + wn * (TN / WN) + t * 16 + grp * 4, g.n, acc[t][u], g.acc);
+    }
+}
+
+template <int TM, int TN, int WM, int WN>
+hipError_t tiled(GemmArgs g, hipStream_t st)
+{
+    g.tiles_m = (int)cdiv(g.m, TM);
+    g.tiles_n = (int)cdiv(g.n, TN);
+    const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n));
+    constexpr int th = WM * WN * 64;
+    if (g.b1)
+        g.bf ? k_gemm_tile<TM, TN, WM, WN, true, true><<<grid, th, 0, st>>>(g)
+             : k_gemm_tile<TM, TN, WM, WN, true, false><<<grid, th, 0, st>>>(g);
+    else
+        g.bf ? k_gemm_tile<TM, TN, WM, WN, false, true><<<grid, th, 0, st>>>(g)
+             : k_gemm_tile<TM, TN, WM, WN, false, false><<<grid, th, 0, st>>>(g);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t gemm_workspace(const GemmArgs&) { return 0; }
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st)
 {
-    if (g.m <= 16)
+    if (g.m <= 16 || g.k == 0)
         return few<1, 1, 8>(g, st);
-    return few<4, 2, 4>(g, st);
+    if (g.m <= 64)
+        return few<4, 2, 4>(g, st);
+    if (cdiv(g.m, 256) * cdiv(g.n, 256) >= 256)
+        return tiled<256, 256, 4, 2>(g, st);
+    return tiled<128, 128, 2, 2>(g, st);
 }
 
 }  // namespace fq

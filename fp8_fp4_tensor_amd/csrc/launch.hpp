@@ -200,6 +200,7 @@ struct GemmArgs {
     int b1 = 0, bf = 0, acc = 0;     // acc: C += (fp32 only)
     int pow2 = 0;                    // every scale is a power of two of at least 2^-127
     float* ws = nullptr;
+    int tiles_m = 0, tiles_n = 0;    // set by the launcher
 };
 // Workspace bytes of a product of this shape (m, n, k, b1 and bf set).
 size_t gemm_workspace(const GemmArgs& g);
