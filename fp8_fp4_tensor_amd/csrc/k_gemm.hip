@@ -104,116 +104,72 @@ __device__ __forceinline__ void store4(void* c, int64_t i, int64_t j, int64_t n,
     }
 }
 
-// Few rows of A (m <= 16 * MT): one workgroup computes 16 * NT columns; its
-// waves take the blocks of k in turn and their sums meet in LDS, in wave
-// order. Nothing is reused but A (from L2), so operands go straight from
-// memory to the matrix unit's registers.
-template <int MT, int NT, int NW, bool B1, bool BF>
-__global__ __launch_bounds__(NW * 64) void k_gemm_few(GemmArgs g)
+// Few rows of A (m <= 16) and no more columns than the chip holds at once: one
+// workgroup computes 16 columns; its waves take the blocks of k in turn and
+// their sums meet in LDS, in wave order. Nothing is reused but A (from L2),
+// so operands go straight from memory to the matrix unit's registers; the
+// loads of 32 waves a CU hide each other's latency (a block fetched ahead in
+// registers measured slower: 6.6 us for 1x4096x4096 against 5.4).
+constexpr int kFewWaves = 8;
+
+template <bool B1, bool BF>
+__global__ __launch_bounds__(kFewWaves * 64) void k_gemm_few(GemmArgs g)
 {
-    __shared__ f32x4 part[NW][MT * NT][64];
+    __shared__ f32x4 part[kFewWaves][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int row = lane & 15, grp = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
-    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int nb = (int)(g.k >> 7);
-    const uint8_t *pa[MT], *pb[NT];
-    const float *psa[MT], *psb[NT];
+    // rows and columns past the last repeat it and are not stored
+    const int64_t i = min((int64_t)row, g.m - 1), j = min(n0 + row, g.n - 1);
+    const uint8_t* pa = g.a + i * g.k + grp * 16;
+    const uint8_t* pb = g.b + j * g.k + grp * 16;
+    const float* psa = g.sa + i * nb;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = w; b < nb; b += kFewWaves) {
+        const i32x8 fb = join(ld16_stream(pb + (int64_t)b * 128), ld16_stream(pb + (int64_t)b * 128 + 64));
+        const i32x8 fa = join(ld16(pa + (int64_t)b * 128), ld16(pa + (int64_t)b * 128 + 64));
+        const float sa = psa[b];
+        float sb[4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int64_t i = min(m0 + t * 16 + row, g.m - 1);  // rows past m repeat the last one and are not stored
-        pa[t] = g.a + i * g.k + grp * 16;
-        psa[t] = g.sa + i * nb;
+        for (int e = 0; e < 4; ++e)
+            sb[e] = B1 ? g.sb[min(n0 + grp * 4 + e, g.n - 1) * nb + b] : g.sb[(n0 >> 7) * nb + b];
+        const f32x4 p = mfma_block<BF>(fb, fa);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] = __builtin_fmaf(p[e], sa * sb[e], acc[e]);
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int64_t j = min(n0 + t * 16 + row, g.n - 1);
-        pb[t] = g.b + j * g.k + grp * 16;
-        psb[t] = B1 ? nullptr : g.sb + (min(n0 + t * 16, g.n - 1) >> 7) * nb;
-    }
-    f32x4 acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-            acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b = w; b < nb; b += NW) {
-        i32x8 fa[MT], fb[NT];
-        float s[MT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            fb[t] = join(ld16_stream(pb[t] + (int64_t)b * 128), ld16_stream(pb[t] + (int64_t)b * 128 + 64));
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            fa[t] = join(ld16(pa[t] + (int64_t)b * 128), ld16(pa[t] + (int64_t)b * 128 + 64));
-            s[t] = psa[t][b];
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if constexpr (B1) {
-                float sb[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sb[e] = g.sb[min(n0 + t * 16 + grp * 4 + e, g.n - 1) * nb + b];
-#pragma unroll
-                for (int u = 0; u < MT; ++u) {
-                    const f32x4 p = mfma_block<BF>(fb[t], fa[u]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[t][u][e] = __builtin_fmaf(p[e], s[u] * sb[e], acc[t][u][e]);
-                }
-            } else {
-                const float sb = psb[t][b];
-#pragma unroll
-                for (int u = 0; u < MT; ++u) {
-                    const f32x4 p = mfma_block<BF>(fb[t], fa[u]);
-                    const float c = s[u] * sb;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[t][u][e] = __builtin_fmaf(p[e], c, acc[t][u][e]);
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-            part[w][t * MT + u][lane] = acc[t][u];
+    part[w][lane] = acc;
     __syncthreads();
-    for (int q = w; q < MT * NT; q += NW) {
-        f32x4 v = part[0][q][lane];
+    if (w > 0 || row >= g.m)
+        return;
 #pragma unroll
-        for (int x = 1; x < NW; ++x)
-            v += part[x][q][lane];
-        const int t = q / MT, u = q - t * MT;
-        const int64_t i = m0 + u * 16 + row;
-        if (i < g.m)
-            store4<BF>(g.c, i, n0 + t * 16 + grp * 4, g.n, v, g.acc);
-    }
+    for (int x = 1; x < kFewWaves; ++x)
+        acc += part[x][lane];
+    store4<BF>(g.c, row, n0 + grp * 4, g.n, acc, g.acc);
 }
 
-template <int MT, int NT, int NW>
 hipError_t few(const GemmArgs& g, hipStream_t st)
 {
-    const dim3 grid((unsigned)cdiv(g.n, 16 * NT), (unsigned)cdiv(g.m, 16 * MT));
+    const dim3 grid((unsigned)cdiv(g.n, 16));
+    constexpr int th = kFewWaves * 64;
     if (g.b1)
-        g.bf ? k_gemm_few<MT, NT, NW, true, true><<<grid, NW * 64, 0, st>>>(g)
-             : k_gemm_few<MT, NT, NW, true, false><<<grid, NW * 64, 0, st>>>(g);
+        g.bf ? k_gemm_few<true, true><<<grid, th, 0, st>>>(g) : k_gemm_few<true, false><<<grid, th, 0, st>>>(g);
     else
-        g.bf ? k_gemm_few<MT, NT, NW, false, true><<<grid, NW * 64, 0, st>>>(g)
-             : k_gemm_few<MT, NT, NW, false, false><<<grid, NW * 64, 0, st>>>(g);
+        g.bf ? k_gemm_few<false, true><<<grid, th, 0, st>>>(g) : k_gemm_few<false, false><<<grid, th, 0, st>>>(g);
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- many rows
+// ---------------------------------------------------------------- tiles
 // One workgroup computes a TM x TN tile of C, WM x WN waves of
-// (TM/WM) x (TN/WN). A step is one scale block: TM + TN rows of 128 bytes
-// come straight from memory into LDS (16 bytes a lane, no registers), one
-// step ahead of the products. The 16-byte chunk c of row r is kept at chunk
-// c ^ (r % 8) of its row, so that eight lanes reading one chunk of eight rows
-// meet no bank twice; the transfer writes LDS in lane order, so it is the
-// lane's source address that carries the permutation.
+// (TM/WM) x (TN/WN), over all blocks of k or, where tiles are few, over a
+// share of them (SPLIT: fp32 partial sums, joined by k_gemm_join). A step is
+// one scale block: TM + TN rows of 128 bytes come straight from memory into
+// one of NS stages of LDS (16 bytes a lane, no registers), NS - 1 steps ahead
+// of the products. The 16-byte chunk c of row r is kept at chunk c ^ (r % 8)
+// of its row, so that eight lanes reading one chunk of eight rows meet no bank
+// twice; the transfer writes LDS in lane order, so it is the lane's source
+// address that carries the permutation.
 
 // 64 lanes' 16 (or 4) bytes each -> LDS at `to`, in lane order. Written as
 // assembly because the compiler, which cannot tell the two stages apart,
@@ -252,42 +208,52 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int64_t& tm, int64_t&
     tm = band * 8 + (in - (uint32_t)tn * high);
 }
 
-template <int TM, int TN, int WM, int WN, bool B1, bool BF>
+template <int TM, int TN, int WM, int WN, int NS, bool B1>
 struct Tile {
     static constexpr int kNW = WM * WN;
     static constexpr int kMT = TM / WM / 16, kNT = TN / WN / 16;
     static_assert(B1 || TN / WN <= 128, "a wave's columns share a 128x128 scale");
+    // transfers a wave issues for a step: eight rows each, and 64 scales
+    static constexpr int kIA = TM / 8 / kNW, kIB = TN / 8 / kNW, kPieces = kIA + kIB + 1;
+    static constexpr int kSA = (TM + 63) / 64, kSB = B1 ? TN / 64 : 1;
+    static_assert(TM % (8 * kNW) == 0 && TN % (8 * kNW) == 0, "whole transfers");
+    static_assert(kNW >= kSA + kSB, "a wave brings 64 scales");
+    static_assert(kPieces * (NS - 2) < 64, "outstanding transfers are counted in six bits");
     struct alignas(1024) Stage {
         uint8_t a[TM * 128], b[TN * 128];
-        float sa[TM], sb[B1 ? TN : 64];
+        float sa[kSA * 64], sb[kSB * 64];
     };
 };
 
-template <int TM, int TN, int WM, int WN, bool B1, bool BF>
+template <int TM, int TN, int WM, int WN, int NS, bool SPLIT, bool B1, bool BF>
 __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
 {
-    using T = Tile<TM, TN, WM, WN, B1, BF>;
-    constexpr int NW = T::kNW, MT = T::kMT, NT = T::kNT;
-    constexpr int IA = TM / 8 / NW, IB = TN / 8 / NW;  // transfers of 8 rows a wave issues
-    static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole transfers");
-    __shared__ typename T::Stage stage[2];
+    using T = Tile<TM, TN, WM, WN, NS, B1>;
+    constexpr int MT = T::kMT, NT = T::kNT, IA = T::kIA, IB = T::kIB, kPieces = T::kPieces;
+    __shared__ typename T::Stage stage[NS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, grp = lane >> 4;
     int64_t tm, tn;
     tile_of(g, tm, tn);
     const int64_t m0 = tm * TM, n0 = tn * TN;
     const int nb = (int)(g.k >> 7);
+    // this workgroup's blocks of k: [first, last)
+    const int first = SPLIT ? (int)((int64_t)nb * blockIdx.y / gridDim.y) : 0;
+    const int last = SPLIT ? (int)((int64_t)nb * (blockIdx.y + 1) / gridDim.y) : nb;
     const int rows_a = (int)min((int64_t)TM, g.m - m0), rows_b = (int)min((int64_t)TN, g.n - n0);
     const uint8_t* pa = g.a + m0 * g.k;
     const uint8_t* pb = g.b + n0 * g.k;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)pa, 0, (int)(rows_a * g.k), 0x00020000);
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)pb, 0, (int)(rows_b * g.k), 0x00020000);
-    const __amdgpu_buffer_rsrc_t rsa =
-        __builtin_amdgcn_make_buffer_rsrc((void*)(g.sa + m0 * nb), 0, rows_a * nb * 4, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(g.sb + (B1 ? n0 : n0 >> 7) * nb), 0, (B1 ? rows_b : (rows_b + 127) >> 7) * nb * 4, 0x00020000);
+    // the scales of one block: the first waves bring A's, the next ones B's;
+    // a wave that is left over repeats a transfer, so that all count the same
+    const bool of_a = w < T::kSA;
+    const int slot = of_a ? w : w < T::kSA + T::kSB ? w - T::kSA : 0;
+    const int rows_s = of_a ? rows_a : B1 ? rows_b : (rows_b + 127) >> 7;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(of_a ? g.sa + m0 * nb : g.sb + (B1 ? n0 : n0 >> 7) * nb), 0, rows_s * nb * 4, 0x00020000);
     // rows past the last repeat it, so every source address is inside; they are not stored
-    int va[IA], vb[IB], vsa, vsb;
+    int va[IA], vb[IB];
     const int sub = lane >> 3, chunk = (lane & 7) ^ sub;
 #pragma unroll
     for (int i = 0; i < IA; ++i)
@@ -295,22 +261,19 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
 #pragma unroll
     for (int i = 0; i < IB; ++i)
         vb[i] = min((w * IB + i) * 8 + sub, rows_b - 1) * (int)g.k + chunk * 16;
-    vsa = min(w * 64 + lane, rows_a - 1) * nb * 4;
-    vsb = min((w - TM / 64) * 64 + lane, (B1 ? rows_b : (rows_b + 127) >> 7) - 1) * nb * 4;
-
+    const int vs = min(slot * 64 + lane, rows_s - 1) * nb * 4;
     const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)stage;
-    auto fill = [&](int which, int b) {
+    // Part of the transfer of block b into a stage: `piece` 0 .. IA + IB - 1
+    // is eight rows of B or A, the last one the scales.
+    auto fill = [&](int which, int b, int piece) {
         const uint32_t to = at + which * (uint32_t)sizeof(typename T::Stage);
-#pragma unroll
-        for (int i = 0; i < IB; ++i)
-            to_lds<16>(rb, to + offsetof(typename T::Stage, b) + (w * IB + i) * 1024, vb[i], b * 128);
-#pragma unroll
-        for (int i = 0; i < IA; ++i)
-            to_lds<16>(ra, to + (w * IA + i) * 1024, va[i], b * 128);
-        if (w < TM / 64)
-            to_lds<4>(rsa, to + offsetof(typename T::Stage, sa) + w * 256, vsa, b * 4);
-        else if (w < TM / 64 + (B1 ? TN / 64 : 1))
-            to_lds<4>(rsb, to + offsetof(typename T::Stage, sb) + (w - TM / 64) * 256, vsb, b * 4);
+        if (piece < IB)
+            to_lds<16>(rb, to + offsetof(typename T::Stage, b) + (w * IB + piece) * 1024, vb[piece < IB ? piece : 0], b * 128);
+        else if (piece < IB + IA)
+            to_lds<16>(ra, to + (w * IA + piece - IB) * 1024, va[piece - IB < IA ? piece - IB : 0], b * 128);
+        else
+            to_lds<4>(rs, to + (of_a ? offsetof(typename T::Stage, sa) : offsetof(typename T::Stage, sb)) + slot * 256, vs,
+                      b * 4);
     };
     const int wm = w / WN, wn = w % WN;
     const int c0 = ((grp ^ (row & 7)) * 16), c1 = c0 ^ 64;
@@ -321,7 +284,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
         for (int u = 0; u < MT; ++u)
             acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto work = [&](const typename T::Stage& s) {
+    auto work = [&](const typename T::Stage& s, int which, int next) {
         i32x8 fa[MT];
         float sc[MT];
         const float sbv = s.sb[wn * (TN / WN) / 128];  // 128x128 tiles: one scale for the wave's columns
@@ -334,15 +297,18 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
             if constexpr (!B1)
                 sc[u] *= sbv;
         }
-        // the next column tile's operand is read during this one's products;
-        // the fences keep the scheduler from reading them all at once, which
-        // would not fit the registers
+        // The next column tile's operand is read during this one's products.
+        // The fences keep the scheduler from reading all of them at once,
+        // which would not fit the registers. The next block's transfers go out
+        // over the first half of the step: all at once, their issue holds up
+        // this step's reads of LDS (8192x4096x14336: 493 us; spread over the
+        // half 455, a quarter 464, the whole step 482: they arrive late).
         i32x8 fb = join(ld16(qb + c0), ld16(qb + c1));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            i32x8 next = fb;
+            i32x8 nx = fb;
             if (t + 1 < NT)
-                next = join(ld16(qb + (t + 1) * 2048 + c0), ld16(qb + (t + 1) * 2048 + c1));
+                nx = join(ld16(qb + (t + 1) * 2048 + c0), ld16(qb + (t + 1) * 2048 + c1));
             f32x4 sb4;
             if constexpr (B1)
                 sb4 = *(const f32x4*)&s.sb[wn * (TN / WN) + t * 16 + grp * 4];
@@ -353,59 +319,222 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
                 for (int e = 0; e < 4; ++e)
                     acc[t][u][e] = __builtin_fmaf(p[e], B1 ? sc[u] * sb4[e] : sc[u], acc[t][u][e]);
             }
-            fb = next;
+            fb = nx;
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (NS == 2) {
+#pragma unroll
+                for (int i = min(2 * t * kPieces / NT, kPieces); i < min(2 * (t + 1) * kPieces / NT, kPieces); ++i)
+                    fill(which, next, i);
+            }
         }
     };
-    // Each wave waits for its own transfers before the barrier; after it the
-    // step's stage is whole, and every wave has read the other one.
-    fill(0, 0);
-    for (int b = 0; b < nb; ++b) {
+    // Each wave waits for its own transfers of the step before the barrier;
+    // after it the step's stage is whole, and every wave has read the stage
+    // that the next transfers overwrite.
+    if constexpr (NS == 2) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            fill(0, first, i);
+        for (int b = first; b < last; ++b) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            // the last step fetches its own block again, unused: without the
+            // branch the step is one run of code
+            work(stage[(b - first) & 1], (b - first + 1) & 1, min(b + 1, last - 1));
+        }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (b + 1 < nb)
-            fill((b + 1) & 1, b + 1);
-        work(stage[b & 1]);
+    } else {
+#pragma unroll
+        for (int p = 0; p < NS - 1; ++p)
+            if (first + p < last) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    fill(p, first + p, i);
+            }
+        int here = 0, there = NS - 1;
+        for (int b = first; b < last; ++b) {
+            if (b + NS - 1 <= last)  // NS - 1 blocks are under way: all but the oldest may stay so
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPieces*(NS - 2)) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (b + NS - 1 < last) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    fill(there, b + NS - 1, i);
+            }
+            work(stage[here], 0, 0);
+            here = here + 1 == NS ? 0 : here + 1;
+            there = there + 1 == NS ? 0 : there + 1;
+        }
     }
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int64_t i = m0 + wm * (TM / WM) + u * 16 + row;
         if (i < g.m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                store4<BF>(g.c, i, n0 + wn * (TN / WN) + t * 16 + grp * 4, g.n, acc[t][u], g.acc);
+            for (int t = 0; t < NT; ++t) {
+                const int64_t j = n0 + wn * (TN / WN) + t * 16 + grp * 4;
+                if constexpr (SPLIT)
+                    store4<false>(g.ws + (int64_t)blockIdx.y * g.m * g.n, i, j, g.n, acc[t][u], false);
+                else
+                    store4<BF>(g.c, i, j, g.n, acc[t][u], g.acc);
+            }
     }
 }
 
-template <int TM, int TN, int WM, int WN>
-hipError_t tiled(GemmArgs g, hipStream_t st)
+// C = the sum of the splits' partial results, in their order (zeros for k = 0,
+// which has none); four values a thread.
+template <bool BF>
+__global__ __launch_bounds__(kWG) void k_gemm_join(GemmArgs g, int splits)
+{
+    const int64_t total = g.m * g.n;
+    const int64_t e = ((int64_t)blockIdx.x * kWG + threadIdx.x) * 4;
+    if (e >= total)
+        return;
+    if (total % 4) {  // partial results are not 16-byte aligned
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (e + i >= total)
+                return;
+            float v = 0.0f;
+            for (int s = 0; s < splits; ++s)
+                v += g.ws[s * total + e + i];
+            if constexpr (BF)
+                ((uint16_t*)g.c)[e + i] = (uint16_t)bf16_bits(v);
+            else
+                ((float*)g.c)[e + i] = g.acc ? ((float*)g.c)[e + i] + v : v;
+        }
+        return;
+    }
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s)
+        v += *(const f32x4*)(g.ws + s * total + e);
+    store4<BF>(g.c, 0, e, total, v, g.acc);
+}
+
+hipError_t join(const GemmArgs& g, int splits, hipStream_t st)
+{
+    const unsigned blocks = (unsigned)cdiv(cdiv(g.m * g.n, 4), kWG);
+    g.bf ? k_gemm_join<true><<<blocks, kWG, 0, st>>>(g, splits) : k_gemm_join<false><<<blocks, kWG, 0, st>>>(g, splits);
+    return hipGetLastError();
+}
+
+template <int TM, int TN, int WM, int WN, int NS, bool SPLIT>
+hipError_t run_tiles(const GemmArgs& g, int splits, hipStream_t st)
+{
+    const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)splits);
+    constexpr int th = WM * WN * 64;
+    if (g.b1)
+        g.bf ? k_gemm_tile<TM, TN, WM, WN, NS, SPLIT, true, true><<<grid, th, 0, st>>>(g)
+             : k_gemm_tile<TM, TN, WM, WN, NS, SPLIT, true, false><<<grid, th, 0, st>>>(g);
+    else
+        g.bf ? k_gemm_tile<TM, TN, WM, WN, NS, SPLIT, false, true><<<grid, th, 0, st>>>(g)
+             : k_gemm_tile<TM, TN, WM, WN, NS, SPLIT, false, false><<<grid, th, 0, st>>>(g);
+    return hipGetLastError();
+}
+
+template <int TM, int TN, int WM, int WN, int NS>
+hipError_t tiled(GemmArgs g, int splits, hipStream_t st)
 {
     g.tiles_m = (int)cdiv(g.m, TM);
     g.tiles_n = (int)cdiv(g.n, TN);
-    const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n));
-    constexpr int th = WM * WN * 64;
-    if (g.b1)
-        g.bf ? k_gemm_tile<TM, TN, WM, WN, true, true><<<grid, th, 0, st>>>(g)
-             : k_gemm_tile<TM, TN, WM, WN, true, false><<<grid, th, 0, st>>>(g);
-    else
-        g.bf ? k_gemm_tile<TM, TN, WM, WN, false, true><<<grid, th, 0, st>>>(g)
-             : k_gemm_tile<TM, TN, WM, WN, false, false><<<grid, th, 0, st>>>(g);
-    return hipGetLastError();
+    if (splits <= 1)
+        return run_tiles<TM, TN, WM, WN, NS, false>(g, 1, st);
+    const hipError_t e = run_tiles<TM, TN, WM, WN, NS, true>(g, splits, st);
+    return e == hipSuccess ? join(g, splits, st) : e;
+}
+
+// Which tile, and over how many shares of k. Each tile's time for one step
+// (one block of k), in us, alone on its CU and with as many as fit, measured
+// on products from 64x2048x7168 to 8192x14336x4096 (bf16 output, and fp32
+// with its half-rate products); steps times rounds of workgroups, or the
+// bytes at 5 TB/s where that is longer, plus the join's launch and traffic,
+// ranks the choices. Measured both ways, the tile chosen against the next:
+// 2048x4096x4096 128x128 44.6 us, 256x256 55.8; 3000x4096x4096 256x256 57.2,
+// 128x128 73.6; 512x4096x14336 128x128 in 4 shares 49.8, whole 105, 64x128 in
+// 2 shares 56.1; 16x7168x18432 32x64 in 4 shares 28.2, k_gemm_few 46.6.
+struct TileCost {
+    int tm, tn, per_cu;
+    double alone[2], full[2];  // [bf16, fp32 output]
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 1, {1.80, 3.30}, {1.80, 3.30}},
+    {128, 128, 2, {0.94, 1.35}, {1.40, 2.20}},
+    {64, 128, 2, {0.67, 0.90}, {1.25, 1.50}},
+    {64, 64, 3, {0.60, 0.73}, {1.10, 1.30}},
+    {32, 64, 4, {0.42, 0.55}, {1.10, 1.20}},
+};
+constexpr int kTileKinds = 5;
+
+struct GemmPlan {
+    int kind = -1;  // index of kTiles, -1: k_gemm_few
+    int splits = 1;
+};
+
+GemmPlan plan_gemm(const GemmArgs& g)
+{
+    GemmPlan best;
+    const int64_t nb = g.k >> 7;
+    // Few rows, at most a workgroup of k_gemm_few a CU and at most 7 blocks a
+    // wave: one launch and no LDS (1x4096x4096: 5.4 us, 32x64 tiles 7.7;
+    // 1x4096x7168 7.9 and 9.7; beyond it they cross: 1x4096x14336 13.6 and 13.3)
+    if ((g.m <= 16 && g.n <= 4096 && nb <= 56) || (g.m <= 16 && g.n <= 8192 && nb <= 16))
+        return best;
+    constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const int prec = g.bf ? 0 : 1;
+    const double bytes = (double)(g.m + g.n) * g.k + (double)g.m * g.n * (g.bf ? 2 : 4);
+    double least = 0.0;
+    for (int k = 0; k < kTileKinds; ++k) {
+        const TileCost& t = kTiles[k];
+        const int64_t tiles = cdiv(g.m, t.tm) * cdiv(g.n, t.tn);
+        for (int s : kSplits) {
+            if (s > 1 && (nb / s < 2 || tiles >= 1024 || (double)s * g.m * g.n * 4 > 128e6))
+                break;
+            const int64_t per_cu = cdiv(tiles * s, 256);  // workgroups of the busiest CU
+            const int64_t rounds = per_cu / t.per_cu, left = per_cu % t.per_cu;
+            const double one = t.alone[prec], all = t.full[prec];
+            double step = rounds * all;
+            if (left)
+                step += t.per_cu == 1 ? one : one + (all - one) * (left - 1) / (t.per_cu - 1);
+            double us = cdiv(nb, s) * step;
+            us = us > bytes / 5e6 ? us : bytes / 5e6;
+            if (s > 1)
+                us += 3.0 + (double)s * g.m * g.n * 8 / 6e6;
+            if (best.kind < 0 || us < least) {
+                best.kind = k;
+                best.splits = s;
+                least = us;
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
-size_t gemm_workspace(const GemmArgs&) { return 0; }
+size_t gemm_workspace(const GemmArgs& g)
+{
+    if (g.k == 0)
+        return 0;
+    const GemmPlan p = plan_gemm(g);
+    return p.splits > 1 ? (size_t)p.splits * g.m * g.n * sizeof(float) : 0;
+}
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st)
 {
-    if (g.m <= 16 || g.k == 0)
-        return few<1, 1, 8>(g, st);
-    if (g.m <= 64)
-        return few<4, 2, 4>(g, st);
-    if (cdiv(g.m, 256) * cdiv(g.n, 256) >= 256)
-        return tiled<256, 256, 4, 2>(g, st);
-    return tiled<128, 128, 2, 2>(g, st);
+    if (g.k == 0)
+        return join(g, 0, st);
+    const GemmPlan p = plan_gemm(g);
+    switch (p.kind) {
+    case 0: return tiled<256, 256, 4, 2, 2>(g, p.splits, st);
+    case 1: return tiled<128, 128, 2, 2, 2>(g, p.splits, st);
+    case 2: return tiled<64, 128, 1, 4, 3>(g, p.splits, st);
+    case 3: return tiled<64, 64, 1, 4, 3>(g, p.splits, st);
+    case 4: return tiled<32, 64, 1, 4, 3>(g, p.splits, st);
+    default: return few(g, st);
+    }
 }
 
 }  // namespace fq

@@ -60,6 +60,20 @@ def test_product(m, n, k, b_rows, pow2, bf16):
     check(run(a, sa, b, sb, b_rows, bf16, pow2), ref, k, bf16, f"{m}x{n}x{k}")
 
 
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k,b_rows", [
+    (4000, 4096, 256, 128), (4100, 4001, 384, 1),            # the largest tiles, ragged, even and odd block counts
+    (1500, 4096, 384, 128), (2000, 2050, 256, 1),
+    (16, 128, 7296, 128), (3, 515, 8192, 1), (30, 256, 9216, 128), (64, 384, 4224, 128), (100, 129, 6400, 1),
+    (200, 512, 8192, 128), (300, 640, 4096, 128), (1, 8192, 384, 128), (16, 8191, 256, 1), (2, 4224, 1152, 128),
+])
+def test_every_tile_and_split(m, n, k, b_rows, bf16):
+    """Shapes that take each tile size, whole and in shares of k."""
+    rng = np.random.default_rng(m + n + k)
+    a, sa, b, sb = operands(rng, m, n, k, b_rows)
+    check(run(a, sa, b, sb, b_rows, bf16), U.product(a, sa, b, sb, b_rows), k, bf16, f"{m}x{n}x{k}")
+
+
 @pytest.mark.parametrize("m,n,k,b_rows", [(5, 128, 256, 128), (70, 130, 384, 1), (300, 513, 256, 1), (9, 256, 4096, 128)])
 def test_accumulate(m, n, k, b_rows):
     rng = np.random.default_rng(m)
