@@ -32,7 +32,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStep = 64;   // tokens a wave takes at once
 constexpr int kRows = 16;   // query rows of a workgroup
-constexpr int kWaves = 4;
+constexpr int kMaxSplits = 1024;
+constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 
@@ -83,8 +84,27 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const KvSeq& s, int r
     return p;
 }
 
-template <int D, int FMT, bool SPLIT>
-__global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
+// Four dims of an output row from its maximum (base 2), sum and accumulator.
+__device__ __forceinline__ void finish(const AttnArgs& a, int64_t rid, int dim, int d, float top, float sum, f32x4 v)
+{
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
+    *(u32x2*)(a.out + rid * dim + d) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+    if (a.lse && d == 0)
+        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
+}
+
+// Few query rows (one token of a grouped head, or short runs): the waves of a
+// workgroup take the steps of a run of keys in turn and join their results in
+// LDS. Bound by reading the cache once, that is by how much is under way: a
+// wave fetches the next step's keys and values as soon as this step's scores
+// are done (values have two sets of registers, keys one), and page indexes a
+// step before that.
+template <int D, int FMT, int kWaves, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 {
     constexpr int C = D / 64;  // 16-byte chunks of a key row a lane holds
     constexpr int T = D / 16;  // value row tiles
@@ -101,6 +121,17 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
     const int r0 = (int)(ht % (unsigned)a.tiles) * kRows;
     const int split = (int)(ht / (unsigned)a.tiles);
     const int seq = (int)blockIdx.y;
+    const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
+    const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block);
+    int page_k = 0, page_v = 0;
+    auto pages = [&](int t0) {  // held to the table's end
+        page_k = table[min((t0 + (row >> 2) * 16) >> ps, kv.max_pages - 1)];
+        page_v = table[min((t0 + grp * 16) >> ps, kv.max_pages - 1)];
+    };
+    // without a window the first step does not depend on the sequence's
+    // length: its pages are looked up beside it, not after it
+    if (a.window == 0 && kv.max_len > 0)
+        pages(split * a.chunk + w * kStep);
     const KvSeq s = kv_seq(kv, seq);
     const int rows = s.nq * group;
     if (r0 >= rows)
@@ -126,39 +157,45 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
     }
     const float sc2 = a.scale * kLog2e;
     const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
-    const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
-    const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block);
-
     float m = -kInf, l = 0.0f;
     f32x4 o[T];
 #pragma unroll
     for (int t = 0; t < T; ++t)
         o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int t0 = begin + w * kStep; t0 < end; t0 += kWaves * kStep) {
-        // the page of the tokens whose keys this lane loads, and of those it scores
+    // A step's keys (row r: tokens 16 (r / 4) + 4 n + r % 4) and values (this
+    // lane's 16 scored tokens), their scales and whether their page exists.
+    struct Values {
+        u32x4 c[T];
+        float ks, vs;
+        bool ok;
+    };
+    u32x4 kc[4][C];
+    Values val[2];
+    auto load = [&](int t0, Values& v) {
         const int tk = t0 + (row >> 2) * 16, tv = t0 + grp * 16;
-        int pk = table[min(tk >> ps, kv.max_pages - 1)], pv = table[min(tv >> ps, kv.max_pages - 1)];
-        const bool ok_k = pk >= 0 && pk < kv.num_pages, ok_v = pv >= 0 && pv < kv.num_pages;
-        pk = ok_k ? pk : 0;
-        pv = ok_v ? pv : 0;
+        v.ok = page_v >= 0 && page_v < kv.num_pages;
+        const int pk = page_k >= 0 && page_k < kv.num_pages ? page_k : 0, pv = v.ok ? page_v : 0;
         const uint8_t* kp =
             kv.k + (((int64_t)pk * kv.heads + h) * kv.page + (tk & (kv.page - 1)) + (row & 3)) * D + grp * 16;
         const int64_t vt = ((int64_t)pv * kv.heads + h) * kv.page;
         const uint8_t* vp = kv.v + vt * D + (int64_t)row * kv.page + (tv & (kv.page - 1));
         const int64_t blk = (vt >> bs) + ((tv & (kv.page - 1)) >> bs);
-        const float ks = kv.ks[blk];
-        float vs = kv.vs[blk];
-        u32x4 kc[4][C], vc[T];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 kc[n][c] = ld16(kp + n * 4 * D + c * 64);
+        v.ks = kv.ks[blk];
+        v.vs = kv.vs[blk];
+        __builtin_amdgcn_sched_barrier(0);  // loads return in order: keys, which are used first, go first
 #pragma unroll
         for (int t = 0; t < T; ++t)
-            vc[t] = ld16(vp + (int64_t)t * 16 * kv.page);
-
+            v.c[t] = ld16(vp + (int64_t)t * 16 * kv.page);
+    };
+    const int hop = kWaves * kStep;
+    auto step = [&](int t0, Values& v, Values& next) {
+        const int tv = t0 + grp * 16;
         float x[16];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -175,25 +212,25 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
         if (a.softcap > 0.0f) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                x[e] = soft_cap(x[e] * ks * a.scale, a.softcap, inv_cap) * kLog2e;
+                x[e] = soft_cap(x[e] * v.ks * a.scale, a.softcap, inv_cap) * kLog2e;
         } else {
-            const float f = ks * sc2;
+            const float f = v.ks * sc2;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 x[e] *= f;
         }
-        const bool inside = t0 >= sp.lo && t0 + kStep <= end && ok_v && t0 + kStep - 1 <= pos && t0 >= oldest;
+        const bool inside = t0 >= sp.lo && t0 + kStep <= end && v.ok && t0 + kStep - 1 <= pos && t0 >= oldest;
         if (!__all(inside)) {
             // scores of keys that a row does not see go to -inf; values of keys
             // that no row sees (a page's unused or outdated part) to zero, for
             // they may hold anything and 0 * NaN is not 0
-            const int from = max(sp.lo - tv, 0), to = ok_v ? min(end - tv, 16) : 0;
+            const int from = max(sp.lo - tv, 0), to = v.ok ? min(end - tv, 16) : 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const bool see = e >= from && e < to && tv + e <= pos && tv + e >= oldest;
                 x[e] = see ? x[e] : -kInf;
             }
-            vs = from < to ? vs : 0.0f;
+            v.vs = from < to ? v.vs : 0.0f;
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 uint32_t keep = 0;
@@ -202,8 +239,12 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
                     keep |= (d * 4 + b >= from && d * 4 + b < to) ? 0xffu << (8 * b) : 0u;
 #pragma unroll
                 for (int t = 0; t < T; ++t)
-                    vc[t][d] &= keep;
+                    v.c[t][d] &= keep;
             }
+        }
+        if (t0 + hop < end) {
+            load(t0 + hop, next);
+            pages(t0 + 2 * hop);
         }
         float top = x[0];
 #pragma unroll
@@ -211,25 +252,50 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
             top = fmaxf(top, x[e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top);
-        const float mu = mn == -kInf ? 0.0f : mn;  // a row that has seen nothing yet
-        const float alpha = __builtin_amdgcn_exp2f(m - mu);
-        m = mn;
+        // m is a row's reference, not its exact maximum: it follows only where a
+        // score passes it by more than 2^kSlack (and at a row's first score), so
+        // that the accumulators are rarely touched between products. The
+        // probabilities' sums stay below 2^kSlack per term, and rounding is
+        // relative.
+        if (__any(top > m + kSlack)) {
+            const float mn = fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (mn == -kInf ? 0.0f : mn));
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                o[t] *= alpha;
+        }
+        const float mu = m == -kInf ? 0.0f : m;  // a row that has seen nothing yet
         float sum = 0.0f;
         bf16x8 p[2];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const float v = __builtin_amdgcn_exp2f(x[e] - mu);
-            sum += v;
-            p[e >> 3][e & 7] = (__bf16)(v * vs);
+            const float f = __builtin_amdgcn_exp2f(x[e] - mu);
+            sum += f;
+            p[e >> 3][e & 7] = (__bf16)(f * v.vs);
         }
-        l = l * alpha + sum;
+        l += sum;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            o[t] *= alpha;
-            o[t] = mfma(widen8<FMT>(vc[t][0], vc[t][1]), p[0], o[t]);
-            o[t] = mfma(widen8<FMT>(vc[t][2], vc[t][3]), p[1], o[t]);
+            o[t] = mfma(widen8<FMT>(v.c[t][0], v.c[t][1]), p[0], o[t]);
+            o[t] = mfma(widen8<FMT>(v.c[t][2], v.c[t][3]), p[1], o[t]);
         }
+    };
+    int t0 = begin + w * kStep;
+    if (t0 < end) {
+        if (a.window != 0)
+            pages(t0);
+        load(t0, val[0]);
+        pages(t0 + hop);
+    }
+    while (t0 < end) {
+        step(t0, val[0], val[1]);
+        t0 += hop;
+        if (t0 >= end)
+            break;
+        step(t0, val[1], val[0]);
+        t0 += hop;
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -241,52 +307,46 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn(AttnArgs a)
     for (int t = 0; t < T; ++t)
         *(f32x4*)&lds_o[w][row][t * 16 + grp * 4] = o[t];
     __syncthreads();
-    // thread -> row threadIdx / 16, dims (threadIdx % 16) * 4 + 64 i
-    const int orow = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
-    if (r0 + orow >= rows)
-        return;
-    float top = lds_m[0][orow];
+    // a thread takes four dims of a row at a time
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kWaves * 64) {
+        const int orow = i / (D / 4), d = i % (D / 4) * 4;
+        if (r0 + orow >= rows)
+            break;
+        float top = lds_m[0][orow];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i)
-        top = fmaxf(top, lds_m[i][orow]);
-    const float mu = top == -kInf ? 0.0f : top;
-    float f[kWaves], sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        f[i] = __builtin_amdgcn_exp2f(lds_m[i][orow] - mu);
-        sum += lds_l[i][orow] * f[i];
-    }
-    const int ro = r0 + orow;
-    const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    if (!SPLIT && a.lse && d0 == 0)
-        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
-    if (SPLIT && d0 == 0)
-        *(float2*)(a.ws + (rid * a.splits + split) * 2) = make_float2(top, sum);
-    float* part = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + (rid * a.splits + split) * D;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        const int d = d0 + c * 64;
+        for (int k = 1; k < kWaves; ++k)
+            top = fmaxf(top, lds_m[k][orow]);
+        const float mu = top == -kInf ? 0.0f : top;
+        float sum = 0.0f;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i)
-            v += *(const f32x4*)&lds_o[i][orow][d] * f[i];
+        for (int k = 0; k < kWaves; ++k) {
+            const float f = __builtin_amdgcn_exp2f(lds_m[k][orow] - mu);
+            sum += lds_l[k][orow] * f;
+            v += *(const f32x4*)&lds_o[k][orow][d] * f;
+        }
+        const int ro = r0 + orow;
+        const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
         if constexpr (SPLIT) {
-            *(f32x4*)(part + d) = v;
+            if (d == 0)
+                *(float2*)(a.ws + (rid * a.splits + split) * 2) = make_float2(top, sum);
+            *(f32x4*)(a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + (rid * a.splits + split) * D + d) = v;
         } else {
-            uint16_t b[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
-            *(u32x2*)(a.out + rid * D + d) = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+            finish(a, rid, D, d, top, sum, v);
         }
     }
 }
 
-// Joins the partial results of a row's splits, in their order.
+// Joins the partial results of a row's splits: a workgroup a row. The splits'
+// maxima and sums are read side by side; then kParts groups of D / 4 threads
+// add up every kParts-th split's four dims and meet in LDS, in order.
 template <int D>
-__global__ __launch_bounds__(D / 4) void k_attn_join(AttnArgs a)
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
 {
+    constexpr int kCols = D / 4, kParts = 256 / kCols;
+    __shared__ float factor[kMaxSplits];
+    __shared__ f32x4 part[kParts][kCols];
+    __shared__ float red[8];
     const KvArgs& kv = a.kv;
     const int group = a.q_heads / kv.heads;
     const KvSeq s = kv_seq(kv, (int)blockIdx.y);
@@ -299,43 +359,69 @@ __global__ __launch_bounds__(D / 4) void k_attn_join(AttnArgs a)
     const int n = sp.hi > sp.from ? (int)cdiv(sp.hi - sp.from, a.chunk) : 0;
     const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
     const float2* ml = (const float2*)a.ws + rid * a.splits;
-    const float* part = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + rid * a.splits * D + threadIdx.x * 4;
+    const float* from = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + rid * a.splits * D;
+    const int w = threadIdx.x >> 6;
+    float2 v[kMaxSplits / 256];
     float top = -kInf;
-    for (int i = 0; i < n; ++i)
-        top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 256; ++k) {
+        const int i = threadIdx.x + k * 256;
+        v[k] = i < n ? ml[i] : make_float2(-kInf, 0.0f);
+        top = fmaxf(top, v[k].x);
+    }
+    top = max_workgroup(top, red);
     const float mu = top == -kInf ? 0.0f : top;
     float sum = 0.0f;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float f = __builtin_amdgcn_exp2f(ml[i].x - mu);
-        sum += ml[i].y * f;
-        v += *(const f32x4*)(part + (int64_t)i * D) * f;
-    }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    uint16_t b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
-    *(u32x2*)(a.out + rid * D + threadIdx.x * 4) = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
-    if (a.lse && threadIdx.x == 0)
-        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
+    for (int k = 0; k < kMaxSplits / 256; ++k) {
+        const int i = threadIdx.x + k * 256;
+        const float f = __builtin_amdgcn_exp2f(v[k].x - mu);
+        sum += v[k].y * f;
+        if (i < n)
+            factor[i] = f;
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2)
+        sum += __shfl_xor(sum, x);
+    if ((threadIdx.x & 63) == 0)
+        red[4 + w] = sum;
+    __syncthreads();
+    sum = (red[4] + red[5]) + (red[6] + red[7]);
+    const int col = threadIdx.x % kCols, p = threadIdx.x / kCols;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = p; i < n; i += kParts)
+        o += *(const f32x4*)(from + (int64_t)i * D + col * 4) * factor[i];
+    part[p][col] = o;
+    __syncthreads();
+    if (p > 0)
+        return;
+#pragma unroll
+    for (int x = 1; x < kParts; ++x)
+        o += part[x][col];
+    finish(a, rid, D, col * 4, top, sum, o);
 }
 
+#ifndef ONEMAX
+#define ONEMAX 1024
+#endif
 template <int D, int FMT>
 hipError_t run(const AttnArgs& a, hipStream_t st)
 {
     const dim3 grid((unsigned)((int64_t)a.splits * a.tiles * a.kv.heads), (unsigned)a.kv.batch);
     if (a.splits == 1) {
-        k_attn<D, FMT, false><<<grid, kWaves * 64, 0, st>>>(a);
+        if (D <= 128 && a.waves == 8)
+            k_attn<D, FMT, D <= 128 ? 8 : 4, false><<<grid, 512, 0, st>>>(a);
+        else
+            k_attn<D, FMT, 4, false><<<grid, 256, 0, st>>>(a);
         return hipGetLastError();
     }
-    k_attn<D, FMT, true><<<grid, kWaves * 64, 0, st>>>(a);
+    k_attn<D, FMT, 4, true><<<grid, 256, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
     const dim3 jgrid((unsigned)((int64_t)a.kv.max_q * a.q_heads), (unsigned)a.kv.batch);
-    k_attn_join<D><<<jgrid, D / 4, 0, st>>>(a);
+    k_attn_join<D><<<jgrid, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -356,16 +442,23 @@ size_t plan_attention(AttnArgs& a)
     int64_t span = kv.max_len;
     if (a.window > 0 && span > (int64_t)a.window + kv.max_q + kStep)
         span = (int64_t)a.window + kv.max_q + kStep;
-    // one workgroup per tile if the tiles alone fill the chip; else about 1024
-    // workgroups, each with at least a step for each of its waves
-    const int64_t least = kWaves * kStep;
-    int64_t splits = tiles >= 512 ? 1 : cdiv(1024, tiles > 0 ? tiles : 1);
-    int64_t chunk = cdiv(cdiv(span, splits), least) * least;
-    if (chunk < least)
-        chunk = least;
-    splits = cdiv(span, chunk);
+    // One workgroup per tile if the tiles alone fill the chip, else about two
+    // workgroups a CU, each with at least a step for each of its four waves
+    // (4 sequences of up to 131072: 16 splits 164 us, 32 177, 64 169, 128 171;
+    // 64 of up to 8192: one 119 us, two 131, eight 120). A short run of keys
+    // on few tiles stays whole, on eight waves: no second launch.
+    a.waves = 4;
+    int64_t splits = tiles >= 512 ? 1 : cdiv(512, tiles > 0 ? tiles : 1);
+    if (splits > 1 && span <= ONEMAX && kv.dim <= 128) {
+        a.waves = 8;
+        splits = 1;
+    }
+    if (span < 1)
+        span = 1;
+    splits = splits < kMaxSplits ? splits : kMaxSplits;
+    const int64_t chunk = cdiv(cdiv(span, splits), 4 * kStep) * (4 * kStep);
     a.chunk = (int)chunk;
-    a.splits = (int)(splits < 1 ? 1 : splits);
+    a.splits = (int)cdiv(span, chunk);
     if (a.splits == 1)
         return 0;
     return (size_t)(kv.total_q * a.q_heads) * a.splits * (kv.dim + 2) * sizeof(float);

@@ -258,9 +258,10 @@ struct AttnArgs {
     float* lse = nullptr;            // [total_q, q_heads] or null
     float* ws = nullptr;             // partial results of split sequences
     int tiles = 0;                   // row tiles of the longest run of queries
+    int waves = 4;                   // of a workgroup
     int chunk = 0, splits = 1;       // tokens a split, splits of the longest sequence
 };
-// Sets tiles, chunk and splits of a call from its shape alone; returns the workspace bytes.
+// Sets tiles, waves, chunk and splits of a call from its shape alone; returns the workspace bytes.
 size_t plan_attention(AttnArgs& a);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
 
