@@ -68,6 +68,18 @@ __device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
     return cap * (1.0f - 2.0f / (e + 1.0f));
 }
 
+// Max over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48), in every
+// lane: the swaps exchange odd 16-lane rows with even ones, then the halves.
+__device__ __forceinline__ float max_groups(float v)
+{
+    typedef uint32_t pair __attribute__((ext_vector_type(2)));
+    const uint32_t b = __float_as_uint(v);
+    const pair r = __builtin_bit_cast(pair, __builtin_amdgcn_permlane16_swap(b, b, false, false));
+    const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+    const pair h = __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(c, c, false, false));
+    return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+
 // The keys that the rows [r0, r1) of a sequence and head see: [lo, hi), empty
 // if hi <= lo; from is lo rounded down to a step.
 struct Span {
@@ -250,8 +262,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
 #pragma unroll
         for (int e = 1; e < 16; ++e)
             top = fmaxf(top, x[e]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = max_groups(top);
         // m is a row's reference, not its exact maximum: it follows only where a
         // score passes it by more than 2^kSlack (and at a row's first score), so
         // that the accumulators are rarely touched between products. The
@@ -337,6 +348,293 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
     }
 }
 
+// ---------------------------------------------------------------- many rows
+// Prompts and chunks: a workgroup takes 8 waves of 16 RT query rows of one
+// head group and walks over the keys in steps of 64. The step's codes are
+// read once, widened to bf16 once, and shared in LDS; the next step's are
+// under way meanwhile. Bound by the vector unit as much as by the matrix
+// unit: 16 x 64 scores cost 32 matrix instructions (512 cycles) and, at an
+// exponential and five operations each, about as many cycles of softmax, so
+// two waves a SIMD alternate between the two.
+//
+// LDS rows: a token's dims (keys) or a dim's 64 tokens (values, in the cache's
+// own order) in 16-byte chunks. Chunk c of dim d sits at c ^ (d % 8); of token
+// t at c ^ key_turn(t), which differs between the tokens that eight lanes read
+// together (16 (r / 4) + 4 n + r % 4 for r = 0..7 or 8..15).
+__device__ __forceinline__ int key_turn(int t) { return (t & 3) | (t >> 2 & 4); }
+
+template <int D>
+struct KvStage {
+    uint16_t k[kStep * D], v[D * kStep];
+};
+
+// Query rows of a workgroup: 32 a wave, 16 with 256 dims, whose accumulators
+// would not fit twice.
+constexpr int tile_rows(int dim) { return dim == 256 ? 128 : 256; }
+
+template <int D, int FMT>
+__global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
+{
+    constexpr int kTileRows = tile_rows(D), kWaveRows = kTileRows / 8, RT = kWaveRows / 16;
+    constexpr int KK = D / 32, T = D / 16;
+    constexpr int kLoads = D / 64;  // 16-byte chunks of codes a thread brings for a step
+    __shared__ KvStage<D> stage[2];
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int row = lane & 15, grp = lane >> 4;
+    const int group = a.q_heads / kv.heads;
+    const unsigned ht = blockIdx.x / (unsigned)kv.heads;
+    const int h = (int)(blockIdx.x - ht * (unsigned)kv.heads);
+    const int r0 = (a.tiles - 1 - (int)ht) * kTileRows;  // the last rows see the most keys: they start first
+    const int seq = (int)blockIdx.y;
+    const KvSeq s = kv_seq(kv, seq);
+    const int rows = s.nq * group;
+    if (r0 >= rows)
+        return;
+    const Span sp = span_of(a, s, r0, min(r0 + kTileRows, rows), group);
+    // this wave's rows; a wave past the last row does the last row's work and stores nothing
+    const int w0 = min(r0 + w * kWaveRows, rows - 1);
+    const Span ws = span_of(a, s, w0, min(w0 + kWaveRows, rows), group);
+    const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
+    const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block), pm = kv.page - 1;
+
+    bf16x8 q[RT][KK];
+    int pos[RT], oldest[RT];
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+        const int r = min(w0 + u * 16 + row, rows - 1);
+        const int tok = r / group, head = h * group + r % group;
+        pos[u] = s.len - s.nq + tok;
+        oldest[u] = a.window > 0 ? pos[u] - a.window + 1 : -0x7fffffff;
+        const uint16_t* p = a.q + (s.q0 + tok) * a.q_stride + (int64_t)head * D + grp * 8;
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            // a negative scale turns the queries' signs, so that scores rise with their products
+            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+            q[u][k] = __builtin_bit_cast(bf16x8, ld16(p + k * 32) ^ u32x4{flip, flip, flip, flip});
+        }
+    }
+    const float scale = fabsf(a.scale), sc2 = scale * kLog2e;
+    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+
+    float m[RT], l[RT];
+    f32x4 o[RT][T];
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+        m[u] = -kInf;
+        l[u] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            o[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // A step's codes on their way: chunk i of this thread is of the keys
+    // (token, 16 dims) below 4 D, of the values (dim, 16 tokens) above.
+    // Page indexes are looked up a step before that.
+    u32x4 code[kLoads];
+    float ks_next = 0.0f, vs_next = 0.0f;
+    bool ok_next = false, there[kLoads];
+    int page[kLoads], page_s;
+    auto token_of = [&](int i) {
+        const int c = threadIdx.x + i * 512;
+        return c < 4 * D ? c / (D / 16) : (c & 3) * 16;
+    };
+    auto pages = [&](int t0) {  // held to the table's end
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            page[i] = table[min((t0 + token_of(i)) >> ps, kv.max_pages - 1)];
+        page_s = table[min((t0 + grp * 16) >> ps, kv.max_pages - 1)];
+    };
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = threadIdx.x + i * 512, t = t0 + token_of(i);
+            there[i] = page[i] >= 0 && page[i] < kv.num_pages;
+            const int64_t base = ((int64_t)(there[i] ? page[i] : 0) * kv.heads + h) * kv.page;
+            if (c < 4 * D)
+                code[i] = ld16(kv.k + (base + (t & pm)) * D + c % (D / 16) * 16);
+            else
+                code[i] = ld16(kv.v + base * D + (int64_t)((c - 4 * D) >> 2) * kv.page + (t & pm));
+        }
+        const int t = t0 + grp * 16;
+        ok_next = page_s >= 0 && page_s < kv.num_pages;
+        const int64_t blk = (((int64_t)(ok_next ? page_s : 0) * kv.heads + h) * kv.page + (t & pm)) >> bs;
+        ks_next = kv.ks[blk];
+        vs_next = kv.vs[blk];
+    };
+    auto put = [&](KvStage<D>& st, int t0) {
+        const bool whole = t0 >= sp.lo && t0 + kStep <= sp.hi;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = threadIdx.x + i * 512;
+            u32x4 x = code[i];
+            uint16_t* to;
+            int at, sw;
+            if (c < 4 * D) {
+                const int t = c / (D / 16);
+                to = st.k + t * D;
+                at = c % (D / 16) * 2;
+                sw = key_turn(t);
+            } else {
+                const int d = (c - 4 * D) >> 2, t = t0 + (c & 3) * 16;
+                to = st.v + d * kStep;
+                at = (c & 3) * 2;
+                sw = d & 7;
+                // values that no row sees go to zero: they may hold anything, and 0 * NaN is not 0
+                if (!whole || !there[i]) {
+                    const int from = max(sp.lo - t, 0), end = there[i] ? min(sp.hi - t, 16) : 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t keep = 0;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            keep |= (e * 4 + b >= from && e * 4 + b < end) ? 0xffu << (8 * b) : 0u;
+                        x[e] &= keep;
+                    }
+                }
+            }
+            *(bf16x8*)(to + (at ^ sw) * 8) = widen8<FMT>(x[0], x[1]);
+            *(bf16x8*)(to + ((at + 1) ^ sw) * 8) = widen8<FMT>(x[2], x[3]);
+        }
+    };
+
+    auto step = [&](const KvStage<D>& st, int t0, float ks, float vs, bool ok) {
+        if (t0 >= ws.hi || t0 + kStep <= ws.lo)
+            return;  // none of this wave's rows sees these keys
+        const int tv = t0 + grp * 16;
+        f32x4 x[RT][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int t = (row >> 2) * 16 + n * 4 + (row & 3);
+#pragma unroll
+            for (int u = 0; u < RT; ++u)
+                x[u][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+                const bf16x8 kf = *(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn(t)) * 8);
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+                    x[u][n] = mfma(kf, q[u][k], x[u][n]);
+            }
+        }
+        // scores stay products until the exponential: x f - m is one fused
+        // operation, and with f >= 0 the largest x has the largest score
+        // (f > 0 also where no token of the group is seen and its scale may be
+        // anything: a hidden score is -inf times f)
+        const float f = a.softcap > 0.0f ? kLog2e : fmaxf(ks * sc2, 1e-30f);
+        // The row tiles go through the softmax side by side, with two branches
+        // for all of them: their chains of dependent operations overlap.
+        bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok;
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+            inside = inside && t0 + kStep - 1 <= pos[u] && t0 >= oldest[u];
+        if (a.softcap > 0.0f) {
+#pragma unroll
+            for (int u = 0; u < RT; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[u][e >> 2][e & 3] = soft_cap(x[u][e >> 2][e & 3] * ks * scale, a.softcap, inv_cap);
+        }
+        if (!__all(inside)) {
+#pragma unroll
+            for (int u = 0; u < RT; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = tv + e;
+                    const bool see = ok && t >= sp.lo && t < sp.hi && t <= pos[u] && t >= oldest[u];
+                    x[u][e >> 2][e & 3] = see ? x[u][e >> 2][e & 3] : -kInf;
+                }
+        }
+        float top[RT];
+        bool rises = false;
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+            top[u] = x[u][0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e)
+                top[u] = fmaxf(top[u], x[u][e >> 2][e & 3]);
+            top[u] = max_groups(top[u] == -kInf ? -kInf : top[u] * f);
+            rises = rises || top[u] > m[u] + kSlack;
+        }
+        if (__any(rises)) {  // as in k_attn
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                const float mn = fmaxf(m[u], top[u]);
+                const float alpha = __builtin_amdgcn_exp2f(m[u] - (mn == -kInf ? 0.0f : mn));
+                m[u] = mn;
+                l[u] *= alpha;
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    o[u][t] *= alpha;
+            }
+        }
+        bf16x8 p[RT][2];
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+            const float mu = m[u] == -kInf ? 0.0f : m[u];
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][e >> 2][e & 3], f, -mu));
+                sum[e & 3] += y;
+                p[u][e >> 3][e & 7] = (__bf16)(y * vs);
+            }
+            l[u] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int d = t * 16 + row;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bf16x8 vf = *(const bf16x8*)(st.v + d * kStep + ((grp * 2 + k) ^ (d & 7)) * 8);
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+                    o[u][t] = mfma(vf, p[u][k], o[u][t]);
+            }
+        }
+    };
+
+    if (sp.from < sp.hi) {
+        pages(sp.from);
+        fetch(sp.from);
+        pages(sp.from + kStep);
+        put(stage[0], sp.from);
+        float ks = ks_next, vs = vs_next;
+        bool ok = ok_next;
+        int cur = 0;
+        for (int t0 = sp.from; t0 < sp.hi; t0 += kStep) {
+            __syncthreads();  // the step's stage is written, the other one read
+            const bool more = t0 + kStep < sp.hi;
+            if (more) {
+                fetch(t0 + kStep);
+                pages(t0 + 2 * kStep);
+            }
+            // a group of tokens that no row sees has a scale that may be anything
+            const int tv = t0 + grp * 16;
+            step(stage[cur], t0, ks, ok && tv < sp.hi && tv + 16 > sp.lo ? vs : 0.0f, ok);
+            if (more)
+                put(stage[cur ^ 1], t0 + kStep);
+            ks = ks_next;
+            vs = vs_next;
+            ok = ok_next;
+            cur ^= 1;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+        float sum = l[u];
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        const int r = r0 + w * kWaveRows + u * 16 + row;
+        if (r < rows) {
+            const int64_t rid = (s.q0 + r / group) * a.q_heads + h * group + r % group;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                finish(a, rid, D, t * 16 + grp * 4, m[u], sum, o[u][t]);
+        }
+    }
+}
+
 // Joins the partial results of a row's splits: a workgroup a row. The splits'
 // maxima and sums are read side by side; then kParts groups of D / 4 threads
 // add up every kParts-th split's four dims and meet in LDS, in order.
@@ -402,12 +700,13 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
     finish(a, rid, D, col * 4, top, sum, o);
 }
 
-#ifndef ONEMAX
-#define ONEMAX 1024
-#endif
 template <int D, int FMT>
 hipError_t run(const AttnArgs& a, hipStream_t st)
 {
+    if (a.rows > kRows) {
+        k_attn_tile<D, FMT><<<dim3((unsigned)(a.tiles * a.kv.heads), (unsigned)a.kv.batch), 512, 0, st>>>(a);
+        return hipGetLastError();
+    }
     const dim3 grid((unsigned)((int64_t)a.splits * a.tiles * a.kv.heads), (unsigned)a.kv.batch);
     if (a.splits == 1) {
         if (D <= 128 && a.waves == 8)
@@ -437,6 +736,23 @@ size_t plan_attention(AttnArgs& a)
 {
     const KvArgs& kv = a.kv;
     const int64_t group = a.q_heads / kv.heads;
+    // The kernel for many rows, where its workgroups fill the chip and their
+    // rows: a step of 64 keys costs it 2.6 us for up to 256 workgroups, and the
+    // kernel for few rows about 1.2 ns a tile of 16 rows. Measured at 128 dims,
+    // many against few: 2 chunks of 2048 rows, 32 heads, up to 8192 keys 560 and
+    // 1122 us; 8 of 128 rows 93 and 86; 1 of 2048 rows, 8 heads 87 and 36; 64 of
+    // 4 rows, 32 heads over 2 171 and 59.
+    const int64_t wide = tile_rows(kv.dim);
+    const int64_t few_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, kRows);
+    const int64_t many_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, wide);
+    a.rows = kRows;
+    if (cdiv(many_tiles, 256) * 2200 < few_tiles * (kv.dim == 256 ? 2 : 1)) {
+        a.rows = (int)wide;
+        a.tiles = (int)cdiv(kv.max_q * group, wide);
+        a.chunk = kv.max_len;
+        a.splits = 1;
+        return 0;
+    }
     a.tiles = (int)cdiv(kv.max_q * group, kRows);
     const int64_t tiles = (int64_t)kv.batch * kv.heads * a.tiles;
     int64_t span = kv.max_len;
@@ -449,7 +765,7 @@ size_t plan_attention(AttnArgs& a)
     // on few tiles stays whole, on eight waves: no second launch.
     a.waves = 4;
     int64_t splits = tiles >= 512 ? 1 : cdiv(512, tiles > 0 ? tiles : 1);
-    if (splits > 1 && span <= ONEMAX && kv.dim <= 128) {
+    if (splits > 1 && span <= 1024 && kv.dim <= 128) {
         a.waves = 8;
         splits = 1;
     }

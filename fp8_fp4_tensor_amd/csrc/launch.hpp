@@ -257,11 +257,12 @@ struct AttnArgs {
     uint16_t* out = nullptr;         // [total_q, q_heads, dim] bf16
     float* lse = nullptr;            // [total_q, q_heads] or null
     float* ws = nullptr;             // partial results of split sequences
+    int rows = 16;                   // query rows of a workgroup
     int tiles = 0;                   // row tiles of the longest run of queries
     int waves = 4;                   // of a workgroup
     int chunk = 0, splits = 1;       // tokens a split, splits of the longest sequence
 };
-// Sets tiles, waves, chunk and splits of a call from its shape alone; returns the workspace bytes.
+// Sets rows, tiles, waves, chunk and splits of a call from its shape alone; returns the workspace bytes.
 size_t plan_attention(AttnArgs& a);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
 

@@ -549,8 +549,8 @@ fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32
  *   q         [total_q, q_heads, head_dim] bf16, tokens q_stride elements apart
  *   out       [total_q, q_heads, head_dim] bf16, contiguous
  *   lse       [total_q, q_heads] fp32, or NULL
- * Cached tokens that a row of the call sees must have finite codes and
- * scales; what no row of the call sees (a page's unused end, pages that
+ * Cached tokens that a row of the call sees must have finite codes and finite
+ * scales that are not negative; what no row of the call sees (a page's unused end, pages that
  * a window has left behind) may hold anything. Scores, softmax and sums are
  * fp32; probabilities are rounded to bf16 for the product with V.
  */

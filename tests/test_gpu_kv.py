@@ -227,6 +227,13 @@ CASES = [  # fmt, heads, q_heads, dim, page, block, lens, counts, window, softca
     (0, 1, 8, 128, 128, 64, [400, 90, 0, 6], [200, 1, 0, 10], 0, 0.0),
     (0, 8, 8, 128, 64, 64, [500], [300], 0, 0.0),
     (0, 1, 1, 128, 16, 16, [2000], [257], 300, 0.0),
+    # many rows (a workgroup shares the keys): ragged, windows, caps, every head size and format
+    (0, 16, 64, 128, 64, 64, [700, 520, 130, 64], [600, 513, 130, 1], 0, 0.0),
+    (1, 16, 64, 128, 16, 16, [530, 300], [511, 300], 100, 0.0),
+    (0, 32, 64, 64, 128, 32, [700, 40, 515], [450, 33, 515], 0, 25.0),
+    (1, 32, 64, 64, 32, 32, [600, 900, 0], [600, 590, 0], 65, 0.0),
+    (0, 16, 32, 256, 64, 64, [300, 420, 20], [300, 257, 20], 0, 0.0),
+    (1, 32, 32, 256, 256, 128, [600, 140], [511, 130], 33, 30.0),
 ]
 
 
@@ -239,7 +246,21 @@ def test_attention(case):
     plain = filled(rng, fmt, heads, dim, page, block, lens, table, pages)
     q, out, lse = attend(plain, table, lens, counts, q_heads, window, softcap, rng=rng)
     check_attention(plain, table, lens, counts, q_heads, q, out, lse, window, softcap,
-                    every=7 if max(counts) > 20 else 1)
+                    every=(67 if heads > 8 else 7) if max(counts) > 20 else 1)
+
+
+def test_attention_many_rows_where_things_go_wrong():
+    """The kernel for many rows: absent pages, rows before the start, NaN beyond the ends, a negative scale."""
+    rng = np.random.default_rng(60)
+    heads, q_heads, page = 16, 64, 64
+    lens, counts = [500, 300, 0, 520], [520, 290, 300, 515]
+    pages = sum(-(-n // page) for n in lens) + 3
+    table = tables(rng, lens, page, pages)
+    table[0, 2], table[1, 4], table[3, 0] = -7, pages, 0x7fffffff
+    plain = filled(rng, 0, heads, 128, page, 64, lens, table, pages, spread=4.0)
+    q, out, lse = attend(plain, table, lens, counts, q_heads, scale=-0.1, rng=rng)
+    check_attention(plain, table, lens, counts, q_heads, q, out, lse, scale=-0.1, every=61)
+    assert torch.all(out[:20] == 0) and torch.all(lse[810:1110] == -float("inf"))
 
 
 def test_attention_large_scores_and_given_scale():
