@@ -9,10 +9,14 @@
 // holds does not depend on how its tokens were split over calls, but for
 // those.
 //
-// Bound by launch latency for single tokens and by memory for prompts: the
-// new rows are read twice (amax, cast), the second time from cache. One
-// workgroup takes one block of one head, K or V; V's codes turn in LDS,
-// because the cache holds V transposed (k_attn.hip says why).
+// Bound by latency for single tokens (lengths, then page and rows, then the
+// codes) and by memory for prompts. One workgroup takes one block of one head,
+// K or V, and holds its rows in registers between the amax and the cast (a
+// block of up to 8 16-byte loads a thread: 64 tokens of 128 bf16 dims take 4;
+// larger ones are read again, from cache). The cache holds V transposed
+// (k_attn.hip says why): a thread takes four tokens of the same dims, and the
+// converter packs them token by token, so the transposed code words come out
+// of registers with no exchange.
 #include "codec.hpp"
 #include "launch.hpp"
 
@@ -34,103 +38,167 @@ __device__ __forceinline__ float dec1(uint32_t code)
     return FMT == kE4M3 ? dec_e4m3(code) : dec_e5m2(code);
 }
 
-constexpr int kMaxBlock = 128, kMaxDim = 256;
+// Codes c moved to another scale, r the ratio of the old to the new one.
+template <int FMT>
+__device__ __forceinline__ uint32_t move4(uint32_t c, float r)
+{
+    return enc4<FMT>(dec1<FMT>(c & 0xffu), dec1<FMT>(c >> 8 & 0xffu), dec1<FMT>(c >> 16 & 0xffu), dec1<FMT>(c >> 24), r);
+}
+
+constexpr int kHold = 8;
+
+template <typename T, int FMT, bool IS_V>
+__device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, int64_t stride, int blocks_per_seq,
+                                             float* red)
+{
+    constexpr int E = In<T>::kE;
+    const int seq = (int)(blockIdx.x / (unsigned)blocks_per_seq);
+    const int nth = (int)blockIdx.x - seq * blocks_per_seq;
+    const int h = blockIdx.y;
+    const KvSeq s = kv_seq(kv, seq);
+    const int first = s.len - s.nq;  // position of the first new token (below 0: it is not stored)
+    const int start = max(first, 0);
+    const int base = start / kv.block * kv.block + nth * kv.block;
+    const int lo = max(base, start), hi = min(base + kv.block, s.len);
+    if (lo >= hi)
+        return;
+    const int page = kv.table[(int64_t)seq * kv.max_pages + base / kv.page];
+    const int dim = kv.dim, in_page = base & (kv.page - 1);
+    const int at = lo - base, cnt = hi - lo;  // the new tokens of the block
+    const int per_row = dim / E, shift = 31 - __clz(per_row);
+    const T* x = fresh + (s.q0 + lo - first) * stride + (int64_t)h * dim;
+
+    // Load j of this thread. K: 16 bytes of a token, consecutive threads along
+    // the token. V: token j % 4 of a group of four, dims dim_of(j); the groups
+    // run fastest.
+    const int g0 = at >> 2, groups = ((at + cnt - 1) >> 2) - g0 + 1;
+    const int total = IS_V ? groups * per_row * 4 : cnt * per_row;   // loads of the block
+    const int loads = IS_V ? (int)cdiv(groups * per_row, kWG) * 4 : (int)cdiv(total, kWG);
+    auto place = [&](int j, int& tok, int& d) {  // token of the block and first dim; false: none
+        if constexpr (IS_V) {
+            const int u = (int)threadIdx.x + (j >> 2) * kWG, c = u / groups;
+            tok = (g0 + u - c * groups) * 4 + (j & 3);
+            d = c * E;
+            return c < per_row && tok >= at && tok < at + cnt;
+        } else {
+            const int i = (int)threadIdx.x + j * kWG;
+            tok = at + (i >> shift);
+            d = (i & (per_row - 1)) * E;
+            return i < total;
+        }
+    };
+    auto load = [&](int j) {
+        int tok, d;
+        return place(j, tok, d) ? ld16(x + (int64_t)(tok - at) * stride + d) : u32x4{0u, 0u, 0u, 0u};
+    };
+    u32x4 hold[kHold];
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+        hold[j] = j < loads ? load(j) : u32x4{0u, 0u, 0u, 0u};
+    if (page < 0 || page >= kv.num_pages)
+        return;
+    const int64_t tile = ((int64_t)page * kv.heads + h) * kv.page;  // in tokens
+    float* scale = (IS_V ? kv.vs : kv.ks) + (tile + in_page) / kv.block;
+    uint8_t* codes = (IS_V ? kv.v : kv.k) + tile * dim;
+    const float olds = at > 0 ? *scale : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+        a = fmaxf(a, In<T>::absmax16(hold[j]));
+    for (int j = kHold; j < loads; ++j)
+        a = fmaxf(a, In<T>::absmax16(load(j)));
+    a = max_workgroup(a, red);  // (every thread has read the old scale)
+    const int p = scale_exp<FMT>(a);
+    const float mine = __uint_as_float((uint32_t)(p + 127) << 23);
+    const bool grows = at > 0 && mine > olds;
+    const float sc = at > 0 && !grows ? olds : mine;
+    if (threadIdx.x == 0)
+        *scale = sc;
+    // x / s: s is 2^p unless an older, larger scale stands
+    const float inv = sc == mine ? __uint_as_float((uint32_t)(127 - p) << 23) : 1.0f / sc;
+
+    if (grows) {  // the block's older tokens, [0, at), move to the new scale
+        const float r = olds * inv;
+        if constexpr (!IS_V) {
+            uint32_t* c = (uint32_t*)(codes + (int64_t)in_page * dim);
+            for (int i = threadIdx.x; i < at * dim / 4; i += kWG)
+                c[i] = move4<FMT>(c[i], r);
+        } else {
+            // whole words of four tokens, and by bytes the word that new tokens share
+            const int words = (at + 3) >> 2;
+            for (int i = threadIdx.x; i < dim * words; i += kWG) {
+                const int d = i / words, t = (i - d * words) * 4;
+                uint8_t* c = codes + (int64_t)d * kv.page + in_page + t;
+                if (t + 4 <= at) {
+                    *(uint32_t*)c = move4<FMT>(*(uint32_t*)c, r);
+                } else {
+                    for (int b = 0; b < at - t; ++b)
+                        c[b] = enc1<FMT>(dec1<FMT>(c[b]), r);
+                }
+            }
+        }
+    }
+    if constexpr (!IS_V) {
+        auto put = [&](int j, u32x4 v) {
+            int tok, d;
+            if (!place(j, tok, d))
+                return;
+            float f[E];
+            In<T>::unpack(v, f);
+            uint32_t* o = (uint32_t*)(codes + (int64_t)(in_page + tok) * dim + d);
+            if constexpr (E == 8)
+                *(u32x2*)o = u32x2{enc4<FMT>(f[0], f[1], f[2], f[3], inv), enc4<FMT>(f[4], f[5], f[6], f[7], inv)};
+            else
+                *o = enc4<FMT>(f[0], f[1], f[2], f[3], inv);
+        };
+#pragma unroll
+        for (int j = 0; j < kHold; ++j)
+            if (j < loads)
+                put(j, hold[j]);
+        for (int j = kHold; j < loads; ++j)
+            put(j, load(j));
+    } else {
+        auto put = [&](int j, u32x4 v0, u32x4 v1, u32x4 v2, u32x4 v3) {
+            const int u = (int)threadIdx.x + (j >> 2) * kWG, c = u / groups;
+            if (c >= per_row)
+                return;
+            const int t = (g0 + u - c * groups) * 4;
+            const int from = max(at - t, 0), to = min(at + cnt - t, 4);
+            float f0[E], f1[E], f2[E], f3[E];
+            In<T>::unpack(v0, f0);
+            In<T>::unpack(v1, f1);
+            In<T>::unpack(v2, f2);
+            In<T>::unpack(v3, f3);
+            uint8_t* o = codes + (int64_t)(c * E) * kv.page + in_page + t;
+#pragma unroll
+            for (int e = 0; e < E; ++e, o += kv.page) {
+                const uint32_t q = enc4<FMT>(f0[e], f1[e], f2[e], f3[e], inv);
+                if (from == 0 && to == 4) {
+                    *(uint32_t*)o = q;
+                } else {
+                    for (int b = from; b < to; ++b)
+                        o[b] = (uint8_t)(q >> (8 * b));
+                }
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kHold; j += 4)
+            if (j < loads)
+                put(j, hold[j], hold[j + 1], hold[j + 2], hold[j + 3]);
+        for (int j = kHold; j < loads; j += 4)
+            put(j, load(j), load(j + 1), load(j + 2), load(j + 3));
+    }
+}
 
 template <typename T, int FMT>
 __global__ __launch_bounds__(kWG) void k_kv_append(KvArgs kv, const T* knew, int64_t kstride, const T* vnew,
                                                    int64_t vstride, int blocks_per_seq)
 {
     __shared__ float red[4];
-    __shared__ uint8_t turn[kMaxDim * (kMaxBlock + 4)];
-    const int seq = (int)(blockIdx.x / (unsigned)blocks_per_seq);
-    const int nth = (int)blockIdx.x - seq * blocks_per_seq;
-    const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
-    const KvSeq s = kv_seq(kv, seq);
-    const int first = s.len - s.nq;  // position of the first new token (below 0: it is not stored)
-    const int start = max(first, 0);
-    const int base = (start / kv.block + nth) * kv.block;
-    const int lo = max(base, start), hi = min(base + kv.block, s.len);
-    if (lo >= hi)
-        return;
-    const int page = kv.table[(int64_t)seq * kv.max_pages + base / kv.page];
-    if (page < 0 || page >= kv.num_pages)
-        return;
-    const int dim = kv.dim, in_page = base & (kv.page - 1);
-    const int64_t tile = ((int64_t)page * kv.heads + h) * kv.page;  // in tokens
-    float* scale = (is_v ? kv.vs : kv.ks) + (tile + in_page) / kv.block;
-    uint8_t* codes = (is_v ? kv.v : kv.k) + tile * dim;
-    const int64_t stride = is_v ? vstride : kstride;
-    const T* x = (is_v ? vnew : knew) + (s.q0 + lo - first) * stride + (int64_t)h * dim;
-    constexpr int E = In<T>::kE;
-    const int per_row = dim / E, n = (hi - lo) * per_row;
-    const int shift = 31 - __clz(per_row);
-
-    float a = 0.0f;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kWG)
-        a = fmaxf(a, In<T>::absmax16(ld16(x + (i >> shift) * stride + (i & (per_row - 1)) * E)));
-    const float olds = lo > base ? *scale : 0.0f;
-    a = max_workgroup(a, red);
-    const int p = scale_exp<FMT>(a);
-    const float mine = __uint_as_float((uint32_t)(p + 127) << 23);
-    const bool grows = lo > base && mine > olds;
-    const float sc = lo > base && !grows ? olds : mine;
-    __syncthreads();  // every thread has read the old scale
-    if (threadIdx.x == 0)
-        *scale = sc;
-    // x / s: s is 2^p unless an older, larger scale stands
-    const float inv = sc == mine ? __uint_as_float((uint32_t)(127 - p) << 23) : 1.0f / sc;
-
-    if (grows) {  // the block's older tokens move to the new scale
-        const float r = olds * inv;
-        const int old = lo - base;
-        for (int i = threadIdx.x; i < old * dim; i += kWG) {
-            uint8_t* c = is_v ? codes + (int64_t)(i / old) * kv.page + in_page + i % old : codes + (int64_t)in_page * dim + i;
-            *c = enc1<FMT>(dec1<FMT>(*c), r);
-        }
-    }
-    if (!is_v) {
-        uint8_t* q = codes + (int64_t)(in_page + lo - base) * dim;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n; i += kWG) {
-            float f[E];
-            In<T>::unpack(ld16(x + (i >> shift) * stride + (i & (per_row - 1)) * E), f);
-            uint32_t* o = (uint32_t*)(q + (int64_t)i * E);
-#pragma unroll
-            for (int e = 0; e < E; e += 4)
-                o[e / 4] = enc4<FMT>(f[e], f[e + 1], f[e + 2], f[e + 3], inv);
-        }
-        return;
-    }
-    const int at = lo - base, cnt = hi - lo, pitch = kv.block + 4;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kWG) {
-        float f[E];
-        const int t = i >> shift, d = (i & (per_row - 1)) * E;
-        In<T>::unpack(ld16(x + t * stride + d), f);
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const uint32_t w = enc4<FMT>(f[e], f[e + 1], f[e + 2], f[e + 3], inv);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                turn[(d + e + b) * pitch + at + t] = (uint8_t)(w >> (8 * b));
-        }
-    }
-    __syncthreads();
-    uint8_t* q = codes + in_page;
-    if (cnt == kv.block) {
-        const int quads = kv.block >> 2, qs = 31 - __clz(quads);
-        for (int i = threadIdx.x; i < dim * quads; i += kWG) {
-            const int d = i >> qs, c = (i & (quads - 1)) * 4;
-            *(uint32_t*)(q + (int64_t)d * kv.page + c) = *(const uint32_t*)(turn + d * pitch + c);
-        }
-        return;
-    }
-    for (int i = threadIdx.x; i < dim * cnt; i += kWG) {
-        const int d = i / cnt, c = at + i % cnt;
-        q[(int64_t)d * kv.page + c] = turn[d * pitch + c];
-    }
+    if (blockIdx.z == 0)
+        append_block<T, FMT, false>(kv, knew, kstride, blocks_per_seq, red);
+    else
+        append_block<T, FMT, true>(kv, vnew, vstride, blocks_per_seq, red);
 }
 
 template <typename T, int FMT>
