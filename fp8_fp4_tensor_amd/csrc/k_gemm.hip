@@ -229,6 +229,8 @@ template <int TM, int TN, int WM, int WN, int NS, bool SPLIT, bool B1, bool BF>
 __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
 {
     using T = Tile<TM, TN, WM, WN, NS, B1>;
+    // both stages full and few reads of A: see the step
+    constexpr bool kLateA = NS == 2 && T::kNT == 8 && T::kIA <= 4;
     constexpr int MT = T::kMT, NT = T::kNT, IA = T::kIA, IB = T::kIB, kPieces = T::kPieces;
     __shared__ typename T::Stage stage[NS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -284,7 +286,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
         for (int u = 0; u < MT; ++u)
             acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto work = [&](const typename T::Stage& s, int which, int next) {
+    auto work = [&](const typename T::Stage& s, int which, int next, int after) {
         i32x8 fa[MT];
         float sc[MT];
         const float sbv = s.sb[wn * (TN / WN) / 128];  // 128x128 tiles: one scale for the wave's columns
@@ -300,9 +302,10 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
         // The next column tile's operand is read during this one's products.
         // The fences keep the scheduler from reading all of them at once,
         // which would not fit the registers. The next block's transfers go out
-        // over the first half of the step: all at once, their issue holds up
-        // this step's reads of LDS (8192x4096x14336: 493 us; spread over the
-        // half 455, a quarter 464, the whole step 482: they arrive late).
+        // between them: all at once, their issue holds up this step's reads of
+        // LDS (8192x4096x14336 with 256x256 tiles: 493 us; spread over half of
+        // the step 455, the whole step 482, for they arrive late; A a step
+        // earlier 409).
         i32x8 fb = join(ld16(qb + c0), ld16(qb + c1));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -321,7 +324,21 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
             }
             fb = nx;
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (NS == 2) {
+            if constexpr (kLateA) {
+                // B and the scales of the next block first, two pieces a tile;
+                // half way every wave holds its part of A in registers, so that
+                // the A of the block after that can replace it already: a
+                // step and a half to arrive, where the whole of a block
+                // brought at once has one
+                if (t * 2 < IB + 1)
+                    fill(which, next, t * 2 < IB ? t * 2 : IA + IB);
+                if (t * 2 + 1 < IB + 1)
+                    fill(which, next, t * 2 + 1 < IB ? t * 2 + 1 : IA + IB);
+                if (t == NT / 2)
+                    asm volatile("s_barrier" ::: "memory");
+                if (t >= NT / 2 && t - NT / 2 < IA)
+                    fill(which ^ 1, after, IB + t - NT / 2);
+            } else if constexpr (NS == 2) {
 #pragma unroll
                 for (int i = min(2 * t * kPieces / NT, kPieces); i < min(2 * (t + 1) * kPieces / NT, kPieces); ++i)
                     fill(which, next, i);
@@ -335,12 +352,18 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             fill(0, first, i);
+        if constexpr (kLateA) {
+#pragma unroll
+            for (int i = 0; i < IA; ++i)
+                fill(1, min(first + 1, last - 1), IB + i);
+        }
         for (int b = first; b < last; ++b) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            // with kLateA all but the A of the block after next, which went out last
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLateA ? IA : 0) : "memory");
             __syncthreads();
-            // the last step fetches its own block again, unused: without the
-            // branch the step is one run of code
-            work(stage[(b - first) & 1], (b - first + 1) & 1, min(b + 1, last - 1));
+            // the last steps fetch their own block again, unused: without
+            // branches the step is one run of code
+            work(stage[(b - first) & 1], (b - first + 1) & 1, min(b + 1, last - 1), min(b + 2, last - 1));
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     } else {
@@ -363,7 +386,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
                 for (int i = 0; i < kPieces; ++i)
                     fill(there, b + NS - 1, i);
             }
-            work(stage[here], 0, 0);
+            work(stage[here], 0, 0, 0);
             here = here + 1 == NS ? 0 : here + 1;
             there = there + 1 == NS ? 0 : there + 1;
         }
@@ -449,9 +472,9 @@ hipError_t tiled(GemmArgs g, int splits, hipStream_t st)
 // Which tile, and over how many shares of k. Each tile's time for one step
 // (one block of k), in us, alone on its CU and with as many as fit, measured
 // on products from 64x2048x7168 to 8192x14336x4096 (bf16 output, and fp32
-// with its half-rate products); steps times rounds of workgroups, or the
-// bytes at 5 TB/s where that is longer, plus the join's launch and traffic,
-// ranks the choices. Measured both ways, the tile chosen against the next:
+// with its half-rate products); steps times rounds of workgroups and the
+// bytes at 5 TB/s, the longer and a quarter of the other, plus the join's
+// launch and traffic, rank the choices. Measured both ways, the tile chosen against the next:
 // 2048x4096x4096 128x128 44.6 us, 256x256 55.8; 3000x4096x4096 256x256 57.2,
 // 128x128 73.6; 512x4096x14336 128x128 in 4 shares 49.8, whole 105, 64x128 in
 // 2 shares 56.1; 16x7168x18432 32x64 in 4 shares 28.2, k_gemm_few 46.6.
@@ -460,7 +483,7 @@ struct TileCost {
     double alone[2], full[2];  // [bf16, fp32 output]
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1, {1.80, 3.30}, {1.80, 3.30}},
+    {256, 256, 1, {1.75, 3.30}, {1.75, 3.30}},
     {128, 128, 2, {0.94, 1.35}, {1.40, 2.20}},
     {64, 128, 2, {0.67, 0.90}, {1.25, 1.50}},
     {64, 64, 3, {0.60, 0.73}, {1.10, 1.30}},
@@ -498,8 +521,8 @@ GemmPlan plan_gemm(const GemmArgs& g)
             double step = rounds * all;
             if (left)
                 step += t.per_cu == 1 ? one : one + (all - one) * (left - 1) / (t.per_cu - 1);
-            double us = cdiv(nb, s) * step;
-            us = us > bytes / 5e6 ? us : bytes / 5e6;
+            const double work = cdiv(nb, s) * step, read = bytes / 5e6;
+            double us = work > read ? work + read / 4 : read + work / 4;  // overlapped, but not wholly
             if (s > 1)
                 us += 3.0 + (double)s * g.m * g.n * 8 / 6e6;
             if (best.kind < 0 || us < least) {
