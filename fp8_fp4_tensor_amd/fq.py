@@ -144,10 +144,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# the current stream's handle without a Stream object (a microsecond less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 # ---------------------------------------------------------------- descriptors
@@ -328,7 +334,9 @@ class Plane:
         if data.element_size() != 1 or scale.dtype != torch.float32:
             raise TypeError("blockwise planes are 8-bit codes and float32 scales")
         self.data, self.scale = data, scale
+        self._sizes = data.numel(), scale.numel()
         self._c = FqPlane(data.data_ptr(), scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def rowwise(cls, q: Quantized) -> "Plane":
@@ -361,14 +369,15 @@ def _nbytes(ws: Optional[torch.Tensor]) -> int:
 
 def fq_gemm(d: FqGemmDesc, a: Plane, b: Plane, out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
     """out [m, n] = A B^T of two blockwise planes (out += with d.accumulate)."""
-    if a.data.numel() != d.m * d.k or b.data.numel() != d.n * d.k or out.numel() != d.m * d.n:
+    m, n, k = d.m, d.n, d.k
+    nb = k // 128
+    if a._sizes[0] != m * k or b._sizes[0] != n * k or out.numel() != m * n:
         raise ValueError("a is [m, k], b is [n, k] and out is [m, n]")
-    nb = d.k // 128
-    if a.scale.numel() != d.m * nb or b.scale.numel() != (d.n if d.b_block_rows == 1 else d.n // 128) * nb:
+    if a._sizes[1] != m * nb or b._sizes[1] != (n if d.b_block_rows == 1 else n // 128) * nb:
         raise ValueError("a scale for each block of 128 (and for 128 rows of b with b_block_rows 128)")
     if in_dtype_of(out) != d.out_dtype or not out.is_contiguous():
         raise TypeError("out is contiguous and of the descriptor's out_dtype")
-    _check(lib().fq_gemm(ctypes.byref(d), ctypes.byref(a._c), ctypes.byref(b._c), out.data_ptr(),
+    _check(lib().fq_gemm(ctypes.byref(d), a._ref, b._ref, out.data_ptr(),
                          None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_gemm")
 
 
@@ -391,6 +400,7 @@ class KvCache:
         self.heads, self.dim, self.page_tokens, self.pages = heads, dim, page, pages
         self._c = FqKvCache(fmt, heads, dim, page, block_tokens, pages, k.data_ptr(), v.data_ptr(),
                             k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
 
 def alloc_kv_cache(fmt: int, pages: int, heads: int, dim: int, page_tokens: int = 64, block_tokens: int = 64,
@@ -423,15 +433,17 @@ class KvBatch:
         self.total_q, self.max_q, self.max_len = total_q, max_q, max_len
         self._c = FqKvBatch(batch, max_pages, max_q, max_len, total_q, page_table.data_ptr(), seq_lens.data_ptr(),
                             None if q_start is None else q_start.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
 
 def _rows3(t: torch.Tensor, total: int, heads: int, dim: int, what: str) -> int:
     """The token stride of a [total, heads, dim] tensor whose tokens are each contiguous."""
-    if tuple(t.shape) != (total, heads, dim):
+    if t.shape != (total, heads, dim):
         raise ValueError(f"{what} is [total_q, heads, head_dim]")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    tokens, rows, dims = t.stride()
+    if dims != 1 or (heads > 1 and rows != dim):
         raise ValueError(f"{what}: a token's heads are contiguous")
-    return t.stride(0) if total > 1 else heads * dim
+    return tokens if total > 1 else heads * dim
 
 
 def fq_kv_append(cache: KvCache, batch: KvBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
@@ -441,7 +453,7 @@ def fq_kv_append(cache: KvCache, batch: KvBatch, k_new: torch.Tensor, v_new: tor
     dt = in_dtype_of(k_new)
     if v_new.dtype != k_new.dtype:
         raise TypeError("k_new and v_new have one dtype")
-    _check(lib().fq_kv_append(ctypes.byref(cache._c), ctypes.byref(batch._c), dt, k_new.data_ptr(), ks,
+    _check(lib().fq_kv_append(cache._ref, batch._ref, dt, k_new.data_ptr(), ks,
                               v_new.data_ptr(), vs, _stream(stream)), "fq_kv_append")
 
 
@@ -451,7 +463,7 @@ def attention_desc(q_heads: int, scale: float = 0.0, window: int = 0, softcap: f
 
 def fq_attention_workspace(cache: KvCache, batch: KvBatch, d: FqAttentionDesc) -> int:
     n = ctypes.c_size_t()
-    _check(lib().fq_attention_workspace(ctypes.byref(cache._c), ctypes.byref(batch._c), ctypes.byref(d),
+    _check(lib().fq_attention_workspace(cache._ref, batch._ref, ctypes.byref(d),
                                         ctypes.byref(n)), "fq_attention_workspace")
     return n.value
 
@@ -473,6 +485,6 @@ def fq_attention(cache: KvCache, batch: KvBatch, d: FqAttentionDesc, q: torch.Te
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != batch.total_q * d.q_heads
                             or not lse.is_contiguous()):
         raise TypeError("lse is contiguous float32 [total_q, q_heads]")
-    _check(lib().fq_attention(ctypes.byref(cache._c), ctypes.byref(batch._c), ctypes.byref(d), q.data_ptr(),
+    _check(lib().fq_attention(cache._ref, batch._ref, ctypes.byref(d), q.data_ptr(),
                               out.data_ptr(), None if lse is None else lse.data_ptr(),
                               None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_attention")
