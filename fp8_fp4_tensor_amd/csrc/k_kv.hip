@@ -119,15 +119,33 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
 
     if (grows) {  // the block's older tokens, [0, at), move to the new scale
         const float r = olds * inv;
-        if constexpr (!IS_V) {
-            uint32_t* c = (uint32_t*)(codes + (int64_t)in_page * dim);
-            for (int i = threadIdx.x; i < at * dim / 4; i += kWG)
-                c[i] = move4<FMT>(c[i], r);
-        } else {
+        // 16 codes a thread, two loads under way: K's tokens are one run, V's
+        // are runs of 16 in each dim's row, and a rest of less than 16
+        const int runs = IS_V ? at >> 4 : at * (dim >> 4);
+        const int n = IS_V ? runs * dim : runs;
+        auto place16 = [&](int i) {
+            if constexpr (!IS_V)
+                return codes + (int64_t)in_page * dim + i * 16;
+            const int d = i / runs;
+            return codes + (int64_t)d * kv.page + in_page + (i - d * runs) * 16;
+        };
+        auto move16 = [&](u32x4 c) {
+            return u32x4{move4<FMT>(c[0], r), move4<FMT>(c[1], r), move4<FMT>(c[2], r), move4<FMT>(c[3], r)};
+        };
+        for (int i = threadIdx.x; i < n; i += 2 * kWG) {
+            const bool two = i + kWG < n;
+            uint8_t* c0 = place16(i);
+            uint8_t* c1 = two ? place16(i + kWG) : c0;
+            const u32x4 v0 = ld16(c0), v1 = ld16(c1);
+            *(u32x4*)c0 = move16(v0);
+            if (two)
+                *(u32x4*)c1 = move16(v1);
+        }
+        if (IS_V && (at & 15)) {
             // whole words of four tokens, and by bytes the word that new tokens share
-            const int words = (at + 3) >> 2;
+            const int from = at & ~15, words = (at - from + 3) >> 2;
             for (int i = threadIdx.x; i < dim * words; i += kWG) {
-                const int d = i / words, t = (i - d * words) * 4;
+                const int d = i / words, t = from + (i - d * words) * 4;
                 uint8_t* c = codes + (int64_t)d * kv.page + in_page + t;
                 if (t + 4 <= at) {
                     *(uint32_t*)c = move4<FMT>(*(uint32_t*)c, r);
