@@ -604,16 +604,14 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         int cur = 0;
         for (int t0 = sp.from; t0 < sp.hi; t0 += kStep) {
             __syncthreads();  // the step's stage is written, the other one read
-            const bool more = t0 + kStep < sp.hi;
-            if (more) {
-                fetch(t0 + kStep);
-                pages(t0 + 2 * kStep);
-            }
+            // (past the last step these fetch once more, unused: a branch
+            // around them makes the compiler wait for them before the step)
+            fetch(t0 + kStep);
+            pages(t0 + 2 * kStep);
             // a group of tokens that no row sees has a scale that may be anything
             const int tv = t0 + grp * 16;
             step(stage[cur], t0, ks, ok && tv < sp.hi && tv + 16 > sp.lo ? vs : 0.0f, ok);
-            if (more)
-                put(stage[cur ^ 1], t0 + kStep);
+            put(stage[cur ^ 1], t0 + kStep);
             ks = ks_next;
             vs = vs_next;
             ok = ok_next;
