@@ -64,6 +64,7 @@ def test_product(m, n, k, b_rows, pow2, bf16):
 @pytest.mark.parametrize("m,n,k,b_rows", [
     (4000, 4096, 256, 128), (4100, 4001, 384, 1),            # the largest tiles, ragged, even and odd block counts
     (1500, 4096, 384, 128), (2000, 2050, 256, 1),
+    (5000, 4096, 512, 128), (4500, 4097, 384, 1),            # more than a round of them: the rest on smaller tiles
     (16, 128, 7296, 128), (3, 515, 8192, 1), (30, 256, 9216, 128), (64, 384, 4224, 128), (100, 129, 6400, 1),
     (200, 512, 8192, 128), (300, 640, 4096, 128), (1, 8192, 384, 128), (16, 8191, 256, 1), (2, 4224, 1152, 128),
 ])
