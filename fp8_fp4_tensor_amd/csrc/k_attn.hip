@@ -5,10 +5,11 @@
 //
 // The codes become bf16 in registers (exact: both 8-bit formats are subsets
 // of bf16) and meet bf16 queries in v_mfma_f32_16x16x32_bf16; the block
-// scales multiply scores and probabilities in fp32. p * vs is rounded to bf16
-// for the second product, at most 2^-8 of each term, as the bf16 output's own
-// rounding is of their sum; the sum of the unrounded p, the maxima and the
-// accumulators are fp32.
+// scales multiply scores and probabilities in fp32. For the second product
+// p * vs becomes bf16: with many rows one term, off by at most 2^-8 of each
+// p, as the bf16 output's own rounding is of their sum; with few rows two
+// terms, for there the matrix unit has time. The sum of the unrounded p, the
+// maxima and the accumulators are fp32.
 //
 // Layout: no operand crosses lanes. The first product computes S^T = K Q^T,
 // K's tokens as the instruction's rows. A step takes 64 tokens as four row
@@ -278,19 +279,25 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
                 o[t] *= alpha;
         }
         const float mu = m == -kInf ? 0.0f : m;  // a row that has seen nothing yet
+        // p * vs in two bf16 terms: the second product costs twice its matrix
+        // instructions, which reading the cache hides, and keeps 16 bits of p
         float sum = 0.0f;
-        bf16x8 p[2];
+        bf16x8 p[2], rest[2];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const float f = __builtin_amdgcn_exp2f(x[e] - mu);
+            const float f = __builtin_amdgcn_exp2f(x[e] - mu), y = f * v.vs;
             sum += f;
-            p[e >> 3][e & 7] = (__bf16)(f * v.vs);
+            p[e >> 3][e & 7] = (__bf16)y;
+            rest[e >> 3][e & 7] = (__bf16)(y - (float)p[e >> 3][e & 7]);
         }
         l += sum;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            o[t] = mfma(widen8<FMT>(v.c[t][0], v.c[t][1]), p[0], o[t]);
-            o[t] = mfma(widen8<FMT>(v.c[t][2], v.c[t][3]), p[1], o[t]);
+            const bf16x8 lo = widen8<FMT>(v.c[t][0], v.c[t][1]), hi = widen8<FMT>(v.c[t][2], v.c[t][3]);
+            o[t] = mfma(lo, p[0], o[t]);
+            o[t] = mfma(hi, p[1], o[t]);
+            o[t] = mfma(lo, rest[0], o[t]);
+            o[t] = mfma(hi, rest[1], o[t]);
         }
     };
     int t0 = begin + w * kStep;

@@ -552,7 +552,8 @@ fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32
  * Cached tokens that a row of the call sees must have finite codes and finite
  * scales that are not negative; what no row of the call sees (a page's unused end, pages that
  * a window has left behind) may hold anything. Scores, softmax and sums are
- * fp32; probabilities are rounded to bf16 for the product with V.
+ * fp32; probabilities times V's scale are bf16 in the product with V (two
+ * bf16 terms where the call has few rows).
  */
 typedef struct {
     int32_t q_heads;
