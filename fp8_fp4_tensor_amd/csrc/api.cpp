@@ -647,8 +647,6 @@ static fq_status check_gemm(const fq_gemm_desc* d)
         return FQ_E_INVALID;
     if (d->out_dtype != FQ_IN_F32 && d->out_dtype != FQ_IN_BF16)
         return FQ_E_INVALID;
-    if (d->scale_mode != FQ_SCALE_DEFAULT && d->scale_mode != FQ_SCALE_POW2)
-        return FQ_E_INVALID;
     if (d->accumulate != 0 && d->accumulate != 1)
         return FQ_E_INVALID;
     if (d->b_block_rows != 1 && d->b_block_rows != 128)
@@ -672,7 +670,6 @@ static GemmArgs gemm_args(const fq_gemm_desc* d)
     g.b1 = d->b_block_rows == 1;
     g.bf = d->out_dtype == FQ_IN_BF16;
     g.acc = d->accumulate;
-    g.pow2 = d->scale_mode == FQ_SCALE_POW2;
     return g;
 }
 

@@ -483,7 +483,7 @@ struct TileCost {
     double alone[2], full[2];  // [bf16, fp32 output]
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1, {1.75, 3.30}, {1.75, 3.30}},
+    {256, 256, 1, {1.75, 3.60}, {1.75, 3.60}},
     {128, 128, 2, {0.94, 1.35}, {1.40, 2.20}},
     {64, 128, 2, {0.67, 0.90}, {1.25, 1.50}},
     {64, 64, 3, {0.60, 0.73}, {1.10, 1.30}},

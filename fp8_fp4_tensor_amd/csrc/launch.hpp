@@ -198,7 +198,6 @@ struct GemmArgs {
     const float* sb = nullptr;       // [n, k/128] if b1, else [n/128, k/128]
     void* c = nullptr;               // [m, n] fp32, or bf16 if bf
     int b1 = 0, bf = 0, acc = 0;     // acc: C += (fp32 only)
-    int pow2 = 0;                    // every scale is a power of two of at least 2^-127
     float* ws = nullptr;
     int tiles_m = 0, tiles_n = 0;    // set by the launcher
 };

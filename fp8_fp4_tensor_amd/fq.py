@@ -56,7 +56,7 @@ class FqDelayedState(ctypes.Structure):
 
 class FqGemmDesc(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("b_block_rows", ctypes.c_int32),
-                ("scale_mode", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+                ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
 
 
 class FqKvCache(ctypes.Structure):
@@ -348,8 +348,8 @@ class Plane:
 
 
 def gemm_desc(m: int, n: int, k: int, b_block_rows: int = 128, out_dtype: int = FQ_IN_BF16,
-              scale_mode: int = FQ_SCALE_DEFAULT, accumulate: bool = False) -> FqGemmDesc:
-    return FqGemmDesc(m, n, k, b_block_rows, scale_mode, out_dtype, int(accumulate))
+              accumulate: bool = False) -> FqGemmDesc:
+    return FqGemmDesc(m, n, k, b_block_rows, out_dtype, int(accumulate))
 
 
 def fq_gemm_workspace(d: FqGemmDesc) -> int:

@@ -424,7 +424,7 @@ fq_status fq_quantize_noalloc(const fq_desc *desc, const void *x, const fq_quant
  * A: [m, k] codes, scales [m, k/128] (1x128 tiles). B: [n, k] codes, scales
  * [n/128, k/128] (128x128 tiles, b_block_rows = 128, n % 128 == 0) or
  * [n, k/128] (1x128 tiles, b_block_rows = 1). Both are planes as FQ_BLOCK_FP32
- * writes them, so the three products of a linear layer Y = X W^T are
+ * writes them, with either scale mode, so the three products of a linear layer Y = X W^T are
  *   forward  Y  [T,O]   a = X's rowwise plane,  b = W's rowwise plane (128x128)
  *   dgrad    dX [T,I]   a = dY's rowwise plane, b = W's colwise plane (128x128)
  *   wgrad    dW [O,I]   a = dY's colwise plane, b = X's colwise plane (1x128)
@@ -433,9 +433,6 @@ fq_status fq_quantize_noalloc(const fq_desc *desc, const void *x, const fq_quant
  * come from the 8-bit matrix instruction, which keeps each product to about
  * 2^-12 of the largest of its block (1e-5 to 5e-5 of the result, against the
  * output's rounding of 2^-8). Products sa * sb must be finite in fp32.
- *   scale_mode   FQ_SCALE_POW2 declares that every scale of both planes is a
- *                power of two (planes quantized with FQ_SCALE_POW2); the
- *                result is the same sum, the scaling then exact.
  *   accumulate   1: C += the product (FQ_IN_F32 only), 0: C = the product.
  *   k % 128 == 0; m*k, n*k and m*n at most 2^36, k at most 2^23.
  * k = 0 gives zeros (or leaves C with accumulate); m = 0 or n = 0 does nothing.
@@ -444,7 +441,6 @@ fq_status fq_quantize_noalloc(const fq_desc *desc, const void *x, const fq_quant
 typedef struct {
     int64_t m, n, k;
     int32_t b_block_rows; /* 1 or 128 */
-    int32_t scale_mode;   /* fq_scale_mode */
     int32_t out_dtype;    /* fq_in_dtype of C */
     int32_t accumulate;
 } fq_gemm_desc;

@@ -21,10 +21,9 @@ def operands(rng, m, n, k, b_rows, pow2=False):
             U.random_codes(rng, (n, k)), U.random_scales(rng, (n if b_rows == 1 else n // 128, nb), pow2))
 
 
-def run(a, sa, b, sb, b_rows, bf16, pow2=False, out=None, accumulate=False, stream=None):
+def run(a, sa, b, sb, b_rows, bf16, out=None, accumulate=False, stream=None):
     (m, k), n = a.shape, b.shape[0]
-    d = fq.gemm_desc(m, n, k, b_rows, fq.FQ_IN_BF16 if bf16 else fq.FQ_IN_F32,
-                     fq.FQ_SCALE_POW2 if pow2 else fq.FQ_SCALE_DEFAULT, accumulate)
+    d = fq.gemm_desc(m, n, k, b_rows, fq.FQ_IN_BF16 if bf16 else fq.FQ_IN_F32, accumulate)
     if out is None:
         out = torch.full((m, n), float("nan"), dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
     fq.fq_gemm(d, fq.Plane(cuda(a), cuda(sa)), fq.Plane(cuda(b), cuda(sb)), out, fq.alloc_gemm_workspace(d), stream)
@@ -57,7 +56,7 @@ def test_product(m, n, k, b_rows, pow2, bf16):
     rng = np.random.default_rng(m * 1000003 + n * 1009 + k + b_rows)
     a, sa, b, sb = operands(rng, m, n, k, b_rows, pow2)
     ref = U.product(a, sa, b, sb, b_rows)
-    check(run(a, sa, b, sb, b_rows, bf16, pow2), ref, k, bf16, f"{m}x{n}x{k}")
+    check(run(a, sa, b, sb, b_rows, bf16), ref, k, bf16, f"{m}x{n}x{k}")
 
 
 @pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
@@ -109,7 +108,7 @@ def test_zero_and_extreme_codes():
         sa, sb = np.full((m, 4), 0.5, np.float32), np.full((2, 4), 2.0, np.float32)
         sa[:, 1] = zero
         sb[1, 2] = zero
-        check(run(a, sa, b, sb, 128, False, pow2), U.product(a, sa, b, sb, 128), k, False, f"pow2={pow2}")
+        check(run(a, sa, b, sb, 128, False), U.product(a, sa, b, sb, 128), k, False, f"pow2={pow2}")
 
 
 @pytest.mark.parametrize("scale_mode", [fq.FQ_SCALE_DEFAULT, fq.FQ_SCALE_POW2], ids=["fp32", "pow2"])
@@ -130,7 +129,7 @@ def test_linear_layer_three_products(scale_mode):
 
     def one(pa, pb, b_rows, bf16, what):
         m, n, k = pa.data.shape[0], pb.data.shape[0], pa.data.shape[1]
-        d = fq.gemm_desc(m, n, k, b_rows, fq.FQ_IN_BF16 if bf16 else fq.FQ_IN_F32, scale_mode)
+        d = fq.gemm_desc(m, n, k, b_rows, fq.FQ_IN_BF16 if bf16 else fq.FQ_IN_F32)
         out = torch.empty((m, n), dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
         fq.fq_gemm(d, pa, pb, out, fq.alloc_gemm_workspace(d))
         torch.cuda.synchronize()

@@ -23,27 +23,26 @@ def gemm(L, d, a=(B, B), b=(B, B), out=B, ws=None, n=0):
                      ctypes.byref(pb) if pb else None, out, ws, n, None)
 
 
-@pytest.mark.parametrize("m,n,k,rows,out,mode,acc,want", [
-    (-1, 128, 128, 128, 1, 0, 0, fq.FQ_E_INVALID),
-    (1, -128, 128, 128, 1, 0, 0, fq.FQ_E_INVALID),
-    (1, 128, -128, 128, 1, 0, 0, fq.FQ_E_INVALID),
-    (1, 128, 128, 128, 2, 0, 0, fq.FQ_E_INVALID),
-    (1, 128, 128, 128, -1, 0, 0, fq.FQ_E_INVALID),
-    (1, 128, 128, 128, 1, 2, 0, fq.FQ_E_INVALID),
-    (1, 128, 128, 128, 0, 0, 2, fq.FQ_E_INVALID),
-    (1, 128, 128, 64, 1, 0, 0, fq.FQ_E_UNSUPPORTED),
-    (1, 128, 128, 0, 1, 0, 0, fq.FQ_E_UNSUPPORTED),
-    (1, 128, 128, 128, 1, 0, 1, fq.FQ_E_UNSUPPORTED),     # accumulating into bf16
-    (1, 128, 100, 128, 1, 0, 0, fq.FQ_E_SHAPE),
-    (1, 100, 128, 128, 1, 0, 0, fq.FQ_E_SHAPE),           # a 128-row tile cut short
-    (1, 128, (1 << 23) + 128, 128, 1, 0, 0, fq.FQ_E_SHAPE),
-    (1 << 30, 128, 128, 128, 1, 0, 0, fq.FQ_E_SHAPE),
-    (1 << 20, 1 << 20, 128, 128, 1, 0, 0, fq.FQ_E_SHAPE),
-    (0, 128, 128, 128, 1, 0, 0, fq.FQ_OK),
-    (5, 0, 128, 1, 0, 0, 1, fq.FQ_OK),
+@pytest.mark.parametrize("m,n,k,rows,out,acc,want", [
+    (-1, 128, 128, 128, 1, 0, fq.FQ_E_INVALID),
+    (1, -128, 128, 128, 1, 0, fq.FQ_E_INVALID),
+    (1, 128, -128, 128, 1, 0, fq.FQ_E_INVALID),
+    (1, 128, 128, 128, 2, 0, fq.FQ_E_INVALID),
+    (1, 128, 128, 128, -1, 0, fq.FQ_E_INVALID),
+    (1, 128, 128, 128, 0, 2, fq.FQ_E_INVALID),
+    (1, 128, 128, 64, 1, 0, fq.FQ_E_UNSUPPORTED),
+    (1, 128, 128, 0, 1, 0, fq.FQ_E_UNSUPPORTED),
+    (1, 128, 128, 128, 1, 1, fq.FQ_E_UNSUPPORTED),     # accumulating into bf16
+    (1, 128, 100, 128, 1, 0, fq.FQ_E_SHAPE),
+    (1, 100, 128, 128, 1, 0, fq.FQ_E_SHAPE),           # a 128-row tile cut short
+    (1, 128, (1 << 23) + 128, 128, 1, 0, fq.FQ_E_SHAPE),
+    (1 << 30, 128, 128, 128, 1, 0, fq.FQ_E_SHAPE),
+    (1 << 20, 1 << 20, 128, 128, 1, 0, fq.FQ_E_SHAPE),
+    (0, 128, 128, 128, 1, 0, fq.FQ_OK),
+    (5, 0, 128, 1, 0, 1, fq.FQ_OK),
 ])
-def test_gemm_shapes(L, m, n, k, rows, out, mode, acc, want):
-    d = fq.FqGemmDesc(m, n, k, rows, mode, out, acc)
+def test_gemm_shapes(L, m, n, k, rows, out, acc, want):
+    d = fq.FqGemmDesc(m, n, k, rows, out, acc)
     z = ctypes.c_size_t()
     assert L.fq_gemm_workspace(ctypes.byref(d), ctypes.byref(z)) == want
     assert gemm(L, d) == want
