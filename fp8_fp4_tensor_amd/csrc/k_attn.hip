@@ -452,20 +452,28 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
             page[i] = table[min((t0 + token_of(i)) >> ps, kv.max_pages - 1)];
         page_s = table[min((t0 + grp * 16) >> ps, kv.max_pages - 1)];
     };
+    // What an address takes beyond the page: a page's bytes, and this thread's
+    // place in it but for the token (a page holds at most 2^28 bytes of codes).
+    const uint32_t page_bytes = (uint32_t)kv.heads * kv.page * D, page_blocks = (uint32_t)kv.heads * kv.page >> bs;
+    const uint8_t* home[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int c = threadIdx.x + i * 512;
+        home[i] = c < 4 * D ? kv.k + (uint32_t)(h * kv.page * D + c % (D / 16) * 16)
+                            : kv.v + (uint32_t)(h * kv.page * D + ((c - 4 * D) >> 2) * kv.page);
+    }
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int c = threadIdx.x + i * 512, t = t0 + token_of(i);
-            there[i] = page[i] >= 0 && page[i] < kv.num_pages;
-            const int64_t base = ((int64_t)(there[i] ? page[i] : 0) * kv.heads + h) * kv.page;
-            if (c < 4 * D)
-                code[i] = ld16(kv.k + (base + (t & pm)) * D + c % (D / 16) * 16);
-            else
-                code[i] = ld16(kv.v + base * D + (int64_t)((c - 4 * D) >> 2) * kv.page + (t & pm));
+            const int c = threadIdx.x + i * 512, t = (t0 + token_of(i)) & pm;
+            there[i] = (uint32_t)page[i] < (uint32_t)kv.num_pages;
+            code[i] = ld16(home[i] + (uint64_t)(there[i] ? (uint32_t)page[i] : 0u) * page_bytes +
+                           (uint32_t)(c < 4 * D ? t * D : t));
         }
-        const int t = t0 + grp * 16;
-        ok_next = page_s >= 0 && page_s < kv.num_pages;
-        const int64_t blk = (((int64_t)(ok_next ? page_s : 0) * kv.heads + h) * kv.page + (t & pm)) >> bs;
+        ok_next = (uint32_t)page_s < (uint32_t)kv.num_pages;
+        // at most 2^26 scales
+        const uint32_t blk = (ok_next ? (uint32_t)page_s : 0u) * page_blocks +
+                             ((uint32_t)(h * kv.page + ((t0 + grp * 16) & pm)) >> bs);
         ks_next = kv.ks[blk];
         vs_next = kv.vs[blk];
     };
