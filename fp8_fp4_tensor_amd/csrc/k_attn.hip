@@ -364,11 +364,18 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
 // exponential and five operations each, about as many cycles of softmax, so
 // two waves a SIMD alternate between the two.
 //
-// LDS rows: a token's dims (keys) or a dim's 64 tokens (values, in the cache's
-// own order) in 16-byte chunks. Chunk c of dim d sits at c ^ (d % 8); of token
-// t at c ^ key_turn(t), which differs between the tokens that eight lanes read
-// together (16 (r / 4) + 4 n + r % 4 for r = 0..7 or 8..15).
-__device__ __forceinline__ int key_turn(int t) { return (t & 3) | (t >> 2 & 4); }
+// LDS rows: a token's dims (keys) or a dim's 64 tokens (values) in 16-byte
+// chunks, turned so that reads of 16 bytes a lane meet no bank twice. The
+// hardware serves 16 lanes at once, eight of one lane group with eight others
+// of the next. A dim's row is half the banks: tokens 16 g + 8 k .. + 7 are chunk
+// g + 4 k, at (g + 4 k) ^ (d % 8). A token's row is all of them or more (half
+// with 64 dims): chunk c of token t sits at c ^ key_turn(t), which numbers the
+// 16 tokens that are read together (16 (r / 4) + 4 n + r % 4 for r = 0..15).
+template <int D>
+__device__ __forceinline__ int key_turn(int t)
+{
+    return (t & 3) | (t >> 2 & (D == 64 ? 4 : 12));
+}
 
 template <int D>
 struct KvStage {
@@ -484,16 +491,18 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
             const int c = threadIdx.x + i * 512;
             u32x4 x = code[i];
             uint16_t* to;
-            int at, sw;
+            int at, hop, sw;  // its two chunks and their turn
             if (c < 4 * D) {
                 const int t = c / (D / 16);
                 to = st.k + t * D;
                 at = c % (D / 16) * 2;
-                sw = key_turn(t);
+                hop = 1;
+                sw = key_turn<D>(t);
             } else {
                 const int d = (c - 4 * D) >> 2, t = t0 + (c & 3) * 16;
                 to = st.v + d * kStep;
-                at = (c & 3) * 2;
+                at = c & 3;
+                hop = 4;
                 sw = d & 7;
                 // values that no row sees go to zero: they may hold anything, and 0 * NaN is not 0
                 if (!whole || !there[i]) {
@@ -509,7 +518,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
                 }
             }
             *(bf16x8*)(to + (at ^ sw) * 8) = widen8<FMT>(x[0], x[1]);
-            *(bf16x8*)(to + ((at + 1) ^ sw) * 8) = widen8<FMT>(x[2], x[3]);
+            *(bf16x8*)(to + ((at + hop) ^ sw) * 8) = widen8<FMT>(x[2], x[3]);
         }
     };
 
@@ -526,7 +535,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
                 x[u][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < KK; ++k) {
-                const bf16x8 kf = *(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn(t)) * 8);
+                const bf16x8 kf = *(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn<D>(t)) * 8);
 #pragma unroll
                 for (int u = 0; u < RT; ++u)
                     x[u][n] = mfma(kf, q[u][k], x[u][n]);
@@ -601,7 +610,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
             const int d = t * 16 + row;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const bf16x8 vf = *(const bf16x8*)(st.v + d * kStep + ((grp * 2 + k) ^ (d & 7)) * 8);
+                const bf16x8 vf = *(const bf16x8*)(st.v + d * kStep + ((grp + 4 * k) ^ (d & 7)) * 8);
 #pragma unroll
                 for (int u = 0; u < RT; ++u)
                     o[u][t] = mfma(vf, p[u][k], o[u][t]);
