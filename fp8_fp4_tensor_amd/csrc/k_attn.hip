@@ -4,14 +4,14 @@
 //   o = sum_t p_t * vs[block of t] * V_t,  p = softmax of s over the visible t
 //
 // The codes become bf16 in registers (exact: both 8-bit formats are subsets
-// of bf16) and meet bf16 queries in v_mfma_f32_16x16x32_bf16; the block
-// scales multiply scores and probabilities in fp32. For the second product
+// of bf16) and meet bf16 queries in v_mfma_f32_16x16x32_bf16 (32x32x16 with
+// many rows and at most 128 dims); the block scales multiply scores and probabilities in fp32. For the second product
 // p * vs becomes bf16: with many rows one term, off by at most 2^-8 of each
 // p, as the bf16 output's own rounding is of their sum; with few rows two
 // terms, for there the matrix unit has time. The sum of the unrounded p, the
 // maxima and the accumulators are fp32.
 //
-// Layout: no operand crosses lanes. The first product computes S^T = K Q^T,
+// Layout (32x32 tiles: see there): no operand crosses lanes. The first product computes S^T = K Q^T,
 // K's tokens as the instruction's rows. A step takes 64 tokens as four row
 // tiles; row r of tile n is token 16 (r / 4) + 4 n + r % 4, so that the four
 // results a lane gets from each tile are, over the four tiles, 16
@@ -28,6 +28,7 @@ namespace fq {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -62,6 +63,11 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 rows, bf16x8 cols, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, cols, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ f32x16 mfma32(bf16x8 rows, bf16x8 cols, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(rows, cols, c, 0, 0, 0);
+}
+
 // cap * tanh(x / cap), by exp: 1 - 2 / (e^{2y} + 1).
 __device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
 {
@@ -79,6 +85,14 @@ __device__ __forceinline__ float max_groups(float v)
     const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
     const pair h = __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(c, c, false, false));
     return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+
+// Max over lanes l and l ^ 32, in both.
+__device__ __forceinline__ float max_halves(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // The keys that the rows [r0, r1) of a sequence and head see: [lo, hi), empty
@@ -356,40 +370,348 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
 }
 
 // ---------------------------------------------------------------- many rows
-// Prompts and chunks: a workgroup takes 8 waves of 16 RT query rows of one
-// head group and walks over the keys in steps of 64. The step's codes are
-// read once, widened to bf16 once, and shared in LDS; the next step's are
-// under way meanwhile. Bound by the vector unit as much as by the matrix
-// unit: 16 x 64 scores cost 32 matrix instructions (512 cycles) and, at an
-// exponential and five operations each, about as many cycles of softmax, so
-// two waves a SIMD alternate between the two.
+// Prompts and chunks: a workgroup takes 8 waves of 32 query rows of one head
+// group and walks over the keys in steps of 64. The step's codes are read once,
+// widened to bf16 once, and shared in LDS, in two stages; the next step's are
+// under way meanwhile and go to LDS between the second product's instructions.
+// 32x32 tiles: the vector unit can issue beside a v_mfma_f32_32x32x16 for half
+// of its cycles, beside a 16x16x32 not at all, and a lane has one query row to
+// keep statistics of instead of two. A step of a wave is 32 matrix instructions
+// (1024 cycles) and some 240 vector ones with 32 exponentials of 16 cycles
+// (about 1400), of two waves a SIMD: bound by issuing both. 2 chunks of 2048
+// rows, 32 heads over 8, up to 8192 keys: 435 to 448 us, about 985 TFLOP/s (474 with 16x16
+// tiles; 393 without reading LDS, 400 without reading the cache, 375 without
+// the softmax). Half a step's shift between the waves of a SIMD changed nothing.
 //
 // LDS rows: a token's dims (keys) or a dim's 64 tokens (values) in 16-byte
 // chunks, turned so that reads of 16 bytes a lane meet no bank twice. The
-// hardware serves 16 lanes at once, eight of one lane group with eight others
-// of the next. A dim's row is half the banks: tokens 16 g + 8 k .. + 7 are chunk
-// g + 4 k, at (g + 4 k) ^ (d % 8). A token's row is all of them or more (half
-// with 64 dims): chunk c of token t sits at c ^ key_turn(t), which numbers the
-// 16 tokens that are read together (16 (r / 4) + 4 n + r % 4 for r = 0..15).
-template <int D>
-__device__ __forceinline__ int key_turn(int t)
+// hardware serves 16 of 32 lanes at once, and the operand's rows that they read
+// are all different modulo 16. `turn` is that number for LDS rows of 16 chunks
+// (all banks), half of it for 8, where the row's parity picks the half of the
+// banks itself.
+template <int CHUNKS>
+__device__ __forceinline__ int turn(int row)
 {
-    return (t & 3) | (t >> 2 & (D == 64 ? 4 : 12));
+    static_assert(CHUNKS == 8 || CHUNKS == 16, "64 or 128 dims, or 64 tokens");
+    return CHUNKS == 8 ? row >> 1 & 7 : row & 15;
 }
+// The operand row (modulo 16) that token t is: see the step.
+__device__ __forceinline__ int key_row(int t) { return (t & 3) | (t >> 2 & 4) | (t << 1 & 8); }
 
 template <int D>
 struct KvStage {
     uint16_t k[kStep * D], v[D * kStep];
 };
 
-// Query rows of a workgroup: 32 a wave, 16 with 256 dims, whose accumulators
-// would not fit twice.
+// Query rows of a workgroup, eight waves: 32 a wave, 16 with 256 dims.
 constexpr int tile_rows(int dim) { return dim == 256 ? 128 : 256; }
 
 template <int D, int FMT>
 __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
 {
-    constexpr int kTileRows = tile_rows(D), kWaveRows = kTileRows / 8, RT = kWaveRows / 16;
+    static_assert(D <= 128, "256 dims: k_attn_tile256");
+    constexpr int kTileRows = tile_rows(D), kWaveRows = 32, kThreads = 512;
+    constexpr int KK = D / 16, T = D / 32;
+    constexpr int kLoads = 8 * D / kThreads;  // 16-byte chunks of codes a thread brings for a step
+    __shared__ KvStage<D> stage[2];
+    const KvArgs& kv = a.kv;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 31, half = lane >> 5;
+    const int group = a.q_heads / kv.heads;
+    const unsigned ht = blockIdx.x / (unsigned)kv.heads;
+    const int h = (int)(blockIdx.x - ht * (unsigned)kv.heads);
+    const int r0 = (a.tiles - 1 - (int)ht) * kTileRows;  // the last rows see the most keys: they start first
+    const int seq = (int)blockIdx.y;
+    const KvSeq s = kv_seq(kv, seq);
+    const int rows = s.nq * group;
+    if (r0 >= rows)
+        return;
+    const Span sp = span_of(a, s, r0, min(r0 + kTileRows, rows), group);
+    // this wave's rows; a wave past the last row does the last row's work and stores nothing
+    const int w0 = min(r0 + w * kWaveRows, rows - 1);
+    const Span ws = span_of(a, s, w0, min(w0 + kWaveRows, rows), group);
+    const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
+    const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block), pm = kv.page - 1;
+
+    bf16x8 q[KK];
+    const int r = min(w0 + row, rows - 1);
+    const int pos = s.len - s.nq + r / group;
+    const int oldest = a.window > 0 ? pos - a.window + 1 : -0x7fffffff;
+    {
+        const uint16_t* p = a.q + (s.q0 + r / group) * a.q_stride + (int64_t)(h * group + r % group) * D + half * 8;
+        // a negative scale turns the queries' signs, so that scores rise with their products
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+            q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 16) ^ u32x4{flip, flip, flip, flip});
+    }
+    const float scale = fabsf(a.scale), sc2 = scale * kLog2e;
+    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+
+    float m = -kInf, l = 0.0f;
+    f32x16 o[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[t][e] = 0.0f;
+
+    // A step's codes on their way: chunk i of this thread is of the keys
+    // (token, 16 dims) below 4 D, of the values (dim, 16 tokens) above. A lane
+    // looks up the page of tokens 16 (lane % 4) .. + 15, a step before: those of
+    // its values and of a scale that it brings, the keys' for lane / 4 even, else
+    // the values'. Its chunks of keys are of one page in the whole wave.
+    u32x4 code[kLoads];
+    float scale_next = 0.0f;
+    bool ok_next = false;
+    int page;
+    const int mine = (lane & 3) * 16;
+    const float* const scales = lane & 4 ? kv.vs : kv.ks;
+    auto of_keys = [&](int i) { return kLoads > 1 ? i < kLoads / 2 : w < 4; };
+    auto look_up = [&](int t0) { page = table[min((t0 + mine) >> ps, kv.max_pages - 1)]; };  // held to the table's end
+    // a page's bytes (at most 2^28) and scales
+    const uint32_t page_bytes = (uint32_t)kv.heads * kv.page * D, page_blocks = (uint32_t)kv.heads * kv.page >> bs;
+    auto fetch = [&](int t0) {
+        ok_next = (uint32_t)page < (uint32_t)kv.num_pages;
+        const uint32_t held = ok_next ? (uint32_t)page : 0u;
+        const int tv = (t0 + mine) & pm;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = threadIdx.x + i * kThreads;
+            if (of_keys(i)) {
+                const int t = c / (D / 16);
+                const uint32_t p = __builtin_amdgcn_readlane(held, __builtin_amdgcn_readfirstlane(t >> 4));
+                code[i] = ld16(kv.k + (uint64_t)p * page_bytes +
+                               (uint32_t)((h * kv.page + ((t0 + t) & pm)) * D + c % (D / 16) * 16));
+            } else {
+                const uint8_t* from = kv.v + (uint32_t)((h * D + ((c - 4 * D) >> 2)) * kv.page);
+                code[i] = ld16(from + (uint64_t)held * page_bytes + (uint32_t)tv);
+            }
+        }
+        scale_next = scales[held * page_blocks + ((uint32_t)(h * kv.page + tv) >> bs)];  // one of at most 2^26
+    };
+    // The codes on their way -> a stage: first values that no row sees go to
+    // zero, for they may hold anything, and 0 * NaN is not 0; then chunk by chunk.
+    auto clear = [&](int t0) {
+        const int t = t0 + mine;
+        const int from = max(sp.lo - t, 0), end = ok_next ? min(sp.hi - t, 16) : 0;
+        if (__all(from == 0 && end == 16))
+            return;
+        uint32_t keep[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            keep[e] = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                keep[e] |= (e * 4 + b >= from && e * 4 + b < end) ? 0xffu << (8 * b) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                code[i][e] &= of_keys(i) ? ~0u : keep[e];
+    };
+    int to[kLoads][2];  // where this thread's chunks go in a stage
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int c = threadIdx.x + i * kThreads, t = c / (D / 16), d = (c - 4 * D) >> 2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            to[i][k] = of_keys(i) ? t * D + ((c % (D / 16) * 2 + k) ^ turn<D / 8>(key_row(t))) * 8
+                                 : kStep * D + d * kStep + (((c & 3) * 2 + k) ^ turn<8>(d)) * 8;
+    }
+    auto put = [&](KvStage<D>& st, int i, int k) {
+        *(bf16x8*)(st.k + to[i][k]) = widen8<FMT>(code[i][2 * k], code[i][2 * k + 1]);
+    };
+
+    // The first product's row r of tile n is token 32 n + 16 (r / 4 % 2) +
+    // 4 (r / 8) + r % 4, so that a lane's 16 results are consecutive tokens of
+    // one query row, and the first and last eight of them are just the column
+    // operand of two of the second product's instructions.
+    const int krow = (row >> 2 & 1) * 16 + (row >> 3) * 4 + (row & 3);
+    auto step = [&](const KvStage<D>& st, KvStage<D>& next, int t0, float sc, uint64_t oks) {
+        const float kf[2] = {__shfl(sc, half), __shfl(sc, half + 2)};
+        const float vf[2] = {__shfl(sc, half + 4), __shfl(sc, half + 6)};
+        // The operands of the next four instructions are read during these
+        // four; fences keep the compiler from moving the reads to their use.
+        bf16x8 fa[4], fb[4];
+        auto keys = [&](bf16x8* to, int at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = (at + i) >> 1, n = i & 1;
+                to[i] = *(const bf16x8*)(st.k + (n * 32 + krow) * D + ((k * 2 + half) ^ turn<D / 8>(row)) * 8);
+            }
+        };
+        auto values = [&](bf16x8* to, int at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = (at + i) % T * 32 + row, k = (at + i) / T;
+                to[i] = *(const bf16x8*)(st.v + d * kStep + (((k >> 1) * 4 + half * 2 + (k & 1)) ^ turn<8>(d)) * 8);
+            }
+        };
+        f32x16 x[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[n][e] = 0.0f;
+        keys(fa, 0);
+#pragma unroll
+        for (int g = 0; g < KK / 2; ++g) {
+            if (g + 1 < KK / 2)
+                keys(fb, (g + 1) * 4);
+            else
+                values(fb, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i & 1] = mfma32(fa[i], q[g * 2 + (i >> 1)], x[i & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                fa[i] = fb[i];
+        }
+        // scores stay products until the exponential: x f - m is one fused
+        // operation, and with f >= 0 the largest x has the largest score
+        // (f > 0 also where no token of the group is seen and its scale may be
+        // anything: a hidden score is -inf times f)
+        const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && (oks & 15) == 15 && t0 + kStep - 1 <= pos && t0 >= oldest;
+        float f[2] = {kf[0], kf[1]};
+        if (a.softcap > 0.0f) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                f[n] = kLog2e;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[n][e] = soft_cap(x[n][e] * kf[n], a.softcap, inv_cap);
+            }
+        }
+        if (!__all(inside)) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const bool ok = oks >> (half + 2 * n) & 1;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = t0 + n * 32 + half * 16 + e;
+                    x[n][e] = ok && t >= sp.lo && t < sp.hi && t <= pos && t >= oldest ? x[n][e] : -kInf;
+                }
+            }
+        }
+        float top = -kInf;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float v = x[n][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e)
+                v = fmaxf(v, x[n][e]);
+            top = fmaxf(top, v == -kInf ? -kInf : v * f[n]);
+        }
+        top = max_halves(top);
+        if (__any(top > m + kSlack)) {  // as in k_attn
+            const float mn = fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (mn == -kInf ? 0.0f : mn));
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                o[t] *= alpha;
+        }
+        bf16x8 p[4];
+        const float mu = m == -kInf ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][e], f[n], -mu));
+                sum[e & 3] += y;
+                p[n * 2 + (e >> 3)][e & 7] = (__bf16)(y * vf[n]);
+            }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        clear(t0 + kStep);
+#pragma unroll
+        for (int g = 0; g < T; ++g) {
+            if (g + 1 < T)
+                values(fb, (g + 1) * 4);
+            constexpr int kPer = kLoads * 2 / T < 1 ? 1 : kLoads * 2 / T;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[(g * 4 + i) % T] = mfma32(fa[i], p[(g * 4 + i) / T], o[(g * 4 + i) % T]);
+#pragma unroll
+            for (int i = g * kPer; i < (g + 1) * kPer; ++i)
+                put(next, i >> 1, i & 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                fa[i] = fb[i];
+        }
+    };
+    // What a step needs of this lane's scale: of a key block, times the scores'
+    // scale; of a value block, zero where no row sees its tokens, for it may be anything.
+    auto factor = [&](int t0) {
+        const int tv = t0 + mine;
+        const float v = ok_next && tv < sp.hi && tv + 16 > sp.lo ? scale_next : 0.0f;
+        const float k = a.softcap > 0.0f ? scale_next * scale : fmaxf(scale_next * sc2, 1e-30f);
+        return lane & 4 ? v : k;
+    };
+
+    if (sp.from < sp.hi) {
+        look_up(sp.from);
+        fetch(sp.from);
+        look_up(sp.from + kStep);
+        clear(sp.from);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                put(stage[0], i, k);
+        float sc = factor(sp.from);
+        uint64_t oks = __ballot(ok_next);
+        int cur = 0;
+        for (int t0 = sp.from; t0 < sp.hi; t0 += kStep) {
+            __syncthreads();  // the step's stage is written, the other one read
+            // (past the last step these fetch once more, unused: a branch
+            // around them makes the compiler wait for them before the step)
+            fetch(t0 + kStep);
+            look_up(t0 + 2 * kStep);
+            if (t0 < ws.hi && t0 + kStep > ws.lo) {
+                step(stage[cur], stage[cur ^ 1], t0, sc, oks);
+            } else {  // none of this wave's rows sees these keys
+                clear(t0 + kStep);
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        put(stage[cur ^ 1], i, k);
+            }
+            sc = factor(t0 + kStep);
+            oks = __ballot(ok_next);
+            cur ^= 1;
+        }
+    }
+    l += __shfl_xor(l, 32);
+    if (r0 + w * kWaveRows + row < rows) {
+        const int64_t rid = (s.q0 + r / group) * a.q_heads + h * group + r % group;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                finish(a, rid, D, t * 32 + i * 8 + half * 4, m, l,
+                       f32x4{o[t][i * 4], o[t][i * 4 + 1], o[t][i * 4 + 2], o[t][i * 4 + 3]});
+    }
+}
+
+// The same for 256 dims, whose accumulators leave no room for 32 rows a wave
+// at two waves a SIMD: 16 rows a wave and 16x16 tiles (2 chunks of 2048 rows, 16
+// heads over 4, up to 8192 keys: 517 us; 32x32 tiles with one wave a SIMD 627).
+// Score tiles as in k_attn, one block of 16 tokens a lane; tokens 16 g + 8 k
+// .. + 7 of a dim are chunk g + 4 k, so that a read meets no bank twice.
+__device__ __forceinline__ int key_turn256(int t) { return (t & 3) | (t >> 2 & 12); }
+
+template <int FMT>
+__global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
+{
+    constexpr int D = 256, kTileRows = tile_rows(D), kWaveRows = 16;
     constexpr int KK = D / 32, T = D / 16;
     constexpr int kLoads = D / 64;  // 16-byte chunks of codes a thread brings for a step
     __shared__ KvStage<D> stage[2];
@@ -412,35 +734,25 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
     const int32_t* table = kv.table + (int64_t)seq * kv.max_pages;
     const int ps = 31 - __clz(kv.page), bs = 31 - __clz(kv.block), pm = kv.page - 1;
 
-    bf16x8 q[RT][KK];
-    int pos[RT], oldest[RT];
+    bf16x8 q[KK];
+    const int r = min(w0 + row, rows - 1);
+    const int pos = s.len - s.nq + r / group;
+    const int oldest = a.window > 0 ? pos - a.window + 1 : -0x7fffffff;
+    {
+        const uint16_t* p = a.q + (s.q0 + r / group) * a.q_stride + (int64_t)(h * group + r % group) * D + grp * 8;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-    for (int u = 0; u < RT; ++u) {
-        const int r = min(w0 + u * 16 + row, rows - 1);
-        const int tok = r / group, head = h * group + r % group;
-        pos[u] = s.len - s.nq + tok;
-        oldest[u] = a.window > 0 ? pos[u] - a.window + 1 : -0x7fffffff;
-        const uint16_t* p = a.q + (s.q0 + tok) * a.q_stride + (int64_t)head * D + grp * 8;
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-            // a negative scale turns the queries' signs, so that scores rise with their products
-            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-            q[u][k] = __builtin_bit_cast(bf16x8, ld16(p + k * 32) ^ u32x4{flip, flip, flip, flip});
-        }
+        for (int k = 0; k < KK; ++k)
+            q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 32) ^ u32x4{flip, flip, flip, flip});
     }
     const float scale = fabsf(a.scale), sc2 = scale * kLog2e;
     const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
 
-    float m[RT], l[RT];
-    f32x4 o[RT][T];
+    float m = -kInf, l = 0.0f;
+    f32x4 o[T];
 #pragma unroll
-    for (int u = 0; u < RT; ++u) {
-        m[u] = -kInf;
-        l[u] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-            o[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int t = 0; t < T; ++t)
+        o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     // A step's codes on their way: chunk i of this thread is of the keys
     // (token, 16 dims) below 4 D, of the values (dim, 16 tokens) above.
@@ -497,7 +809,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
                 to = st.k + t * D;
                 at = c % (D / 16) * 2;
                 hop = 1;
-                sw = key_turn<D>(t);
+                sw = key_turn256(t);
             } else {
                 const int d = (c - 4 * D) >> 2, t = t0 + (c & 3) * 16;
                 to = st.v + d * kStep;
@@ -526,95 +838,60 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         if (t0 >= ws.hi || t0 + kStep <= ws.lo)
             return;  // none of this wave's rows sees these keys
         const int tv = t0 + grp * 16;
-        f32x4 x[RT][4];
+        f32x4 x[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int t = (row >> 2) * 16 + n * 4 + (row & 3);
+            x[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < RT; ++u)
-                x[u][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < KK; ++k) {
-                const bf16x8 kf = *(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn<D>(t)) * 8);
-#pragma unroll
-                for (int u = 0; u < RT; ++u)
-                    x[u][n] = mfma(kf, q[u][k], x[u][n]);
-            }
+            for (int k = 0; k < KK; ++k)
+                x[n] = mfma(*(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn256(t)) * 8), q[k], x[n]);
         }
-        // scores stay products until the exponential: x f - m is one fused
-        // operation, and with f >= 0 the largest x has the largest score
-        // (f > 0 also where no token of the group is seen and its scale may be
-        // anything: a hidden score is -inf times f)
         const float f = a.softcap > 0.0f ? kLog2e : fmaxf(ks * sc2, 1e-30f);
-        // The row tiles go through the softmax side by side, with two branches
-        // for all of them: their chains of dependent operations overlap.
-        bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok;
-#pragma unroll
-        for (int u = 0; u < RT; ++u)
-            inside = inside && t0 + kStep - 1 <= pos[u] && t0 >= oldest[u];
+        const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok && t0 + kStep - 1 <= pos && t0 >= oldest;
         if (a.softcap > 0.0f) {
 #pragma unroll
-            for (int u = 0; u < RT; ++u)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[u][e >> 2][e & 3] = soft_cap(x[u][e >> 2][e & 3] * ks * scale, a.softcap, inv_cap);
+            for (int e = 0; e < 16; ++e)
+                x[e >> 2][e & 3] = soft_cap(x[e >> 2][e & 3] * ks * scale, a.softcap, inv_cap);
         }
         if (!__all(inside)) {
 #pragma unroll
-            for (int u = 0; u < RT; ++u)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int t = tv + e;
-                    const bool see = ok && t >= sp.lo && t < sp.hi && t <= pos[u] && t >= oldest[u];
-                    x[u][e >> 2][e & 3] = see ? x[u][e >> 2][e & 3] : -kInf;
-                }
-        }
-        float top[RT];
-        bool rises = false;
-#pragma unroll
-        for (int u = 0; u < RT; ++u) {
-            top[u] = x[u][0][0];
-#pragma unroll
-            for (int e = 1; e < 16; ++e)
-                top[u] = fmaxf(top[u], x[u][e >> 2][e & 3]);
-            top[u] = max_groups(top[u] == -kInf ? -kInf : top[u] * f);
-            rises = rises || top[u] > m[u] + kSlack;
-        }
-        if (__any(rises)) {  // as in k_attn
-#pragma unroll
-            for (int u = 0; u < RT; ++u) {
-                const float mn = fmaxf(m[u], top[u]);
-                const float alpha = __builtin_amdgcn_exp2f(m[u] - (mn == -kInf ? 0.0f : mn));
-                m[u] = mn;
-                l[u] *= alpha;
-#pragma unroll
-                for (int t = 0; t < T; ++t)
-                    o[u][t] *= alpha;
-            }
-        }
-        bf16x8 p[RT][2];
-#pragma unroll
-        for (int u = 0; u < RT; ++u) {
-            const float mu = m[u] == -kInf ? 0.0f : m[u];
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][e >> 2][e & 3], f, -mu));
-                sum[e & 3] += y;
-                p[u][e >> 3][e & 7] = (__bf16)(y * vs);
+                const int t = tv + e;
+                const bool see = ok && t >= sp.lo && t < sp.hi && t <= pos && t >= oldest;
+                x[e >> 2][e & 3] = see ? x[e >> 2][e & 3] : -kInf;
             }
-            l[u] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
+        float top = x[0][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e)
+            top = fmaxf(top, x[e >> 2][e & 3]);
+        top = max_groups(top == -kInf ? -kInf : top * f);
+        if (__any(top > m + kSlack)) {
+            const float mn = fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (mn == -kInf ? 0.0f : mn));
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                o[t] *= alpha;
+        }
+        bf16x8 p[2];
+        const float mu = m == -kInf ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 2][e & 3], f, -mu));
+            sum[e & 3] += y;
+            p[e >> 3][e & 7] = (__bf16)(y * vs);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const int d = t * 16 + row;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const bf16x8 vf = *(const bf16x8*)(st.v + d * kStep + ((grp + 4 * k) ^ (d & 7)) * 8);
-#pragma unroll
-                for (int u = 0; u < RT; ++u)
-                    o[u][t] = mfma(vf, p[u][k], o[u][t]);
-            }
+            for (int k = 0; k < 2; ++k)
+                o[t] = mfma(*(const bf16x8*)(st.v + d * kStep + ((grp + 4 * k) ^ (d & 7)) * 8), p[k], o[t]);
         }
     };
 
@@ -642,18 +919,13 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
             cur ^= 1;
         }
     }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (r0 + w * kWaveRows + row < rows) {
+        const int64_t rid = (s.q0 + r / group) * a.q_heads + h * group + r % group;
 #pragma unroll
-    for (int u = 0; u < RT; ++u) {
-        float sum = l[u];
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        const int r = r0 + w * kWaveRows + u * 16 + row;
-        if (r < rows) {
-            const int64_t rid = (s.q0 + r / group) * a.q_heads + h * group + r % group;
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-                finish(a, rid, D, t * 16 + grp * 4, m[u], sum, o[u][t]);
-        }
+        for (int t = 0; t < T; ++t)
+            finish(a, rid, D, t * 16 + grp * 4, m, l, o[t]);
     }
 }
 
@@ -726,7 +998,11 @@ template <int D, int FMT>
 hipError_t run(const AttnArgs& a, hipStream_t st)
 {
     if (a.rows > kRows) {
-        k_attn_tile<D, FMT><<<dim3((unsigned)(a.tiles * a.kv.heads), (unsigned)a.kv.batch), 512, 0, st>>>(a);
+        const dim3 tiles((unsigned)(a.tiles * a.kv.heads), (unsigned)a.kv.batch);
+        if constexpr (D == 256)
+            k_attn_tile256<FMT><<<tiles, 512, 0, st>>>(a);
+        else
+            k_attn_tile<D, FMT><<<tiles, 512, 0, st>>>(a);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)((int64_t)a.splits * a.tiles * a.kv.heads), (unsigned)a.kv.batch);
@@ -759,16 +1035,19 @@ size_t plan_attention(AttnArgs& a)
     const KvArgs& kv = a.kv;
     const int64_t group = a.q_heads / kv.heads;
     // The kernel for many rows, where its workgroups fill the chip and their
-    // rows: a step of 64 keys costs it 2.6 us for up to 256 workgroups, and the
-    // kernel for few rows about 1.2 ns a tile of 16 rows. Measured at 128 dims,
-    // many against few: 2 chunks of 2048 rows, 32 heads, up to 8192 keys 560 and
-    // 1122 us; 8 of 128 rows 93 and 86; 1 of 2048 rows, 8 heads 87 and 36; 64 of
-    // 4 rows, 32 heads over 2 171 and 59.
+    // rows: a step of 64 keys costs it the same up to 256 workgroups, and the
+    // kernel for few rows in proportion to its tiles of 16 rows. They are even at
+    // the tiles below, measured with 32 heads over 8, many against few in us: 128
+    // dims, 8 sequences of 128 rows and up to 2000 keys (2048 tiles) 71 and 88; 6
+    // of them (1536) 70 and 67; 2 of 320 rows and 8192 keys (1280) 252 and 224;
+    // 2 of 400 rows and 2000 keys (1600) 69 and 81; 64 dims, 8 of 128 rows (2048)
+    // 57 and 42; 256 dims, 4 of 128 rows (1024) 86 and 123.
+    const int64_t even = kv.dim == 64 ? 2800 : kv.dim == 128 ? 1600 : 725;
     const int64_t wide = tile_rows(kv.dim);
     const int64_t few_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, kRows);
     const int64_t many_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, wide);
     a.rows = kRows;
-    if (cdiv(many_tiles, 256) * 2200 < few_tiles * (kv.dim == 256 ? 2 : 1)) {
+    if (cdiv(many_tiles, 256) * even < few_tiles) {
         a.rows = (int)wide;
         a.tiles = (int)cdiv(kv.max_q * group, wide);
         a.chunk = kv.max_len;
