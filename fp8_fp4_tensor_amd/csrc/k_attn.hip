@@ -68,11 +68,13 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 rows, bf16x8 cols, f32x16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(rows, cols, c, 0, 0, 0);
 }
 
-// cap * tanh(x / cap), by exp: 1 - 2 / (e^{2y} + 1).
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap)
+// log2(e) cap * tanh(s / cap) = c2 (1 - 2 / (2^{x twice} + 1)): c2 = log2(e) cap,
+// and `twice` turns x into 2 log2(e) s / cap. The reciprocal is the
+// instruction's, off by a unit (an exact division made chunks of 2048 rows, 32
+// heads, up to 8192 keys 865 us; so 567).
+__device__ __forceinline__ float soft_cap(float x, float twice, float c2)
 {
-    const float e = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
-    return cap * (1.0f - 2.0f / (e + 1.0f));
+    return __builtin_fmaf(-2.0f * c2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * twice) + 1.0f), c2);
 }
 
 // Max over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48), in every
@@ -182,8 +184,8 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
             q[c][1] = __builtin_bit_cast(bf16x8, ld16(p + c * 64 + 8));
         }
     }
-    const float sc2 = a.scale * kLog2e;
-    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+    // products to scores, base 2; with a cap to its tanh's argument
+    const float c2 = a.softcap * kLog2e, sc2 = a.scale * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
     float m = -kInf, l = 0.0f;
     f32x4 o[T];
 #pragma unroll
@@ -236,12 +238,12 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
             for (int e = 0; e < 4; ++e)
                 x[n * 4 + e] = d[e];
         }
+        const float f = v.ks * sc2;
         if (a.softcap > 0.0f) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                x[e] = soft_cap(x[e] * v.ks * a.scale, a.softcap, inv_cap) * kLog2e;
+                x[e] = soft_cap(x[e], f, c2);
         } else {
-            const float f = v.ks * sc2;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 x[e] *= f;
@@ -445,8 +447,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         for (int k = 0; k < KK; ++k)
             q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 16) ^ u32x4{flip, flip, flip, flip});
     }
-    const float scale = fabsf(a.scale), sc2 = scale * kLog2e;
-    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+    const float c2 = a.softcap * kLog2e;
+    const float sc2 = fabsf(a.scale) * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
 
     float m = -kInf, l = 0.0f;
     f32x16 o[T];
@@ -580,10 +582,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         if (a.softcap > 0.0f) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                f[n] = kLog2e;
+                f[n] = 1.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    x[n][e] = soft_cap(x[n][e] * kf[n], a.softcap, inv_cap);
+                    x[n][e] = soft_cap(x[n][e], kf[n], c2);
             }
         }
         if (!__all(inside)) {
@@ -651,8 +653,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
     auto factor = [&](int t0) {
         const int tv = t0 + mine;
         const float v = ok_next && tv < sp.hi && tv + 16 > sp.lo ? scale_next : 0.0f;
-        const float k = a.softcap > 0.0f ? scale_next * scale : fmaxf(scale_next * sc2, 1e-30f);
-        return lane & 4 ? v : k;
+        const float k = scale_next * sc2;
+        return lane & 4 ? v : a.softcap > 0.0f ? k : fmaxf(k, 1e-30f);
     };
 
     if (sp.from < sp.hi) {
@@ -745,8 +747,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
         for (int k = 0; k < KK; ++k)
             q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 32) ^ u32x4{flip, flip, flip, flip});
     }
-    const float scale = fabsf(a.scale), sc2 = scale * kLog2e;
-    const float inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
+    const float c2 = a.softcap * kLog2e;
+    const float sc2 = fabsf(a.scale) * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
 
     float m = -kInf, l = 0.0f;
     f32x4 o[T];
@@ -847,12 +849,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
             for (int k = 0; k < KK; ++k)
                 x[n] = mfma(*(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn256(t)) * 8), q[k], x[n]);
         }
-        const float f = a.softcap > 0.0f ? kLog2e : fmaxf(ks * sc2, 1e-30f);
+        const float f = a.softcap > 0.0f ? 1.0f : fmaxf(ks * sc2, 1e-30f);
         const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok && t0 + kStep - 1 <= pos && t0 >= oldest;
         if (a.softcap > 0.0f) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                x[e >> 2][e & 3] = soft_cap(x[e >> 2][e & 3] * ks * scale, a.softcap, inv_cap);
+                x[e >> 2][e & 3] = soft_cap(x[e >> 2][e & 3], ks * sc2, c2);
         }
         if (!__all(inside)) {
 #pragma unroll
