@@ -274,6 +274,23 @@ def test_attention_large_scores_and_given_scale():
         check_attention(plain, table, lens, counts, 4, q, out, lse, scale=scale, every=3)
 
 
+@pytest.mark.parametrize("heads, q_heads, dim, lens, counts", [
+    (1, 4, 128, [300, 70], [1, 1]), (16, 64, 128, [520, 130], [515, 130]), (32, 64, 64, [600, 40], [600, 33]),
+    (16, 32, 256, [300, 20], [300, 20])])
+def test_attention_scales_of_any_size(heads, q_heads, dim, lens, counts):
+    """A cache that something else wrote: scales that are no powers of two, and zeros."""
+    rng = np.random.default_rng(61)
+    page = 64
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = tables(rng, lens, page, pages)
+    plain = filled(rng, 0, heads, dim, page, 32, lens, table, pages)
+    for scales in (plain.ks, plain.vs):
+        scales *= rng.uniform(0.4, 1.7, size=scales.shape).astype(np.float32)
+        scales[rng.random(scales.shape) < 0.1] = 0.0
+    q, out, lse = attend(plain, table, lens, counts, q_heads, rng=rng)
+    check_attention(plain, table, lens, counts, q_heads, q, out, lse, every=67 if heads > 8 else 1)
+
+
 def test_attention_absent_pages():
     """Tokens on pages outside the cache are not seen; a row with no page at all is empty."""
     rng = np.random.default_rng(51)
