@@ -443,7 +443,11 @@ def _rows3(t: torch.Tensor, total: int, heads: int, dim: int, what: str) -> int:
     tokens, rows, dims = t.stride()
     if dims != 1 or (heads > 1 and rows != dim):
         raise ValueError(f"{what}: a token's heads are contiguous")
-    return tokens if total > 1 else heads * dim
+    if total <= 1:
+        return heads * dim
+    if tokens < heads * dim:  # an expanded row's 0 would mean contiguous to the library
+        raise ValueError(f"{what}: tokens do not overlap")
+    return tokens
 
 
 def fq_kv_append(cache: KvCache, batch: KvBatch, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
