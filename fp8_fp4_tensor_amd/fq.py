@@ -480,8 +480,13 @@ def alloc_attention_workspace(cache: KvCache, batch: KvBatch, d: FqAttentionDesc
 
 def fq_attention(cache: KvCache, batch: KvBatch, d: FqAttentionDesc, q: torch.Tensor, out: torch.Tensor,
                  lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
-    """out [total_q, q_heads, dim] bf16 (and lse [total_q, q_heads] fp32) = attention of q over the cache."""
-    d.q_stride = _rows3(q, batch.total_q, d.q_heads, cache.dim, "q")
+    """out [total_q, q_heads, dim] bf16 (and lse [total_q, q_heads] fp32) = attention of q over the cache.
+    The token stride is q's own, whatever d.q_stride holds."""
+    stride = _rows3(q, batch.total_q, d.q_heads, cache.dim, "q")
+    if stride == d.q_heads * cache.dim:
+        stride = 0
+    if stride != d.q_stride:  # a descriptor of this call: the caller's may be in use elsewhere
+        d = FqAttentionDesc(d.q_heads, d.window, d.scale, d.softcap, stride)
     if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise TypeError("q and out are bfloat16")
     if out.shape != q.shape or not out.is_contiguous():

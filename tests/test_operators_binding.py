@@ -42,3 +42,36 @@ def test_tokens_that_overlap_are_refused(rows):
         with pytest.raises(ValueError):
             fq.fq_kv_append(c, b, new.expand(rows, 2, 64) if q.stride(0) == 0 else new.as_strided((rows, 2, 64), (64, 64, 1)),
                             z(rows, 2, 64, dtype=torch.bfloat16), Stream)
+
+
+def test_attention_leaves_the_descriptor_alone(monkeypatch):
+    """One descriptor serves caches of several head dims and queries of several strides, and never holds a
+    call's own stride: another thread, or a workspace query, may be reading it."""
+    seen = []
+    real = fq.lib()
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+        def fq_attention(self, cache, batch, desc, *rest):
+            got = desc._obj
+            seen.append((got.q_heads, got.window, got.scale, got.softcap, got.q_stride))
+            return fq.FQ_OK
+
+    monkeypatch.setattr(fq, "lib", Lib)
+    monkeypatch.setattr(fq, "_one_gpu", lambda *a: None, raising=False)
+    d = fq.attention_desc(4, scale=0.5, window=7, softcap=2.0)
+    for dim, joint in ((64, 4 * 64), (64, 4 * 64 + 128), (128, 4 * 128), (64, 1024), (256, 4 * 256 + 8)):
+        c, b = cache(dim=dim), batch(3)
+        q = z(3, joint, dtype=torch.bfloat16)[:, :4 * dim].view(3, 4, dim)
+        fq.fq_attention(c, b, d, q, torch.empty((3, 4, dim), dtype=torch.bfloat16), None, None, Stream)
+        assert seen[-1] == (4, 7, 0.5, 2.0, 0 if joint == 4 * dim else joint)
+        assert (d.q_heads, d.window, d.scale, d.softcap, d.q_stride) == (4, 7, 0.5, 2.0, 0)
+        for other in (64, 128, 256):
+            fq.fq_attention_workspace(cache(dim=other), b, d)
+    # a stride that the caller has set is not the call's: queries say theirs
+    d.q_stride = 1 << 30
+    fq.fq_attention(cache(), batch(3), d, z(3, 4, 64, dtype=torch.bfloat16), z(3, 4, 64, dtype=torch.bfloat16), None, None,
+                    Stream)
+    assert seen[-1][-1] == 0 and d.q_stride == 1 << 30
