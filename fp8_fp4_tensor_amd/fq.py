@@ -325,7 +325,18 @@ def fq_requantize_transpose(d: FqDesc, src: Quantized, dst: Quantized, stream=No
 
 
 # ---------------------------------------------------------------- operators on 8-bit data
-class Plane:
+class _Handle:
+    """A C struct with the tensors it points into. The struct is filled once, so
+    the attributes are fixed: make another handle for other tensors or sizes."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a {type(self).__name__} is fixed: make another one")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+
+class Plane(_Handle):
     """One quantized copy as an operand: codes and scales (kept alive here)."""
 
     def __init__(self, data: torch.Tensor, scale: torch.Tensor):
@@ -333,10 +344,8 @@ class Plane:
             raise ValueError("planes are contiguous")
         if data.element_size() != 1 or scale.dtype != torch.float32:
             raise TypeError("blockwise planes are 8-bit codes and float32 scales")
-        self.data, self.scale = data, scale
-        self._sizes = data.numel(), scale.numel()
-        self._c = FqPlane(data.data_ptr(), scale.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        c = FqPlane(data.data_ptr(), scale.data_ptr())
+        self.__dict__.update(data=data, scale=scale, _sizes=(data.numel(), scale.numel()), _c=c, _ref=ctypes.byref(c))
 
     @classmethod
     def rowwise(cls, q: Quantized) -> "Plane":
@@ -381,7 +390,7 @@ def fq_gemm(d: FqGemmDesc, a: Plane, b: Plane, out: torch.Tensor, ws: Optional[t
                          None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_gemm")
 
 
-class KvCache:
+class KvCache(_Handle):
     """A paged 8-bit key/value cache (buffers and their shape)."""
 
     def __init__(self, fmt: int, block_tokens: int, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
@@ -395,12 +404,10 @@ class KvCache:
             raise TypeError("codes are 8-bit and scales float32")
         if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
             raise ValueError("cache buffers are contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.fmt, self.block_tokens = fmt, block_tokens
-        self.heads, self.dim, self.page_tokens, self.pages = heads, dim, page, pages
-        self._c = FqKvCache(fmt, heads, dim, page, block_tokens, pages, k.data_ptr(), v.data_ptr(),
-                            k_scale.data_ptr(), v_scale.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        c = FqKvCache(fmt, heads, dim, page, block_tokens, pages, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                      v_scale.data_ptr())
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, fmt=fmt, block_tokens=block_tokens, heads=heads,
+                             dim=dim, page_tokens=page, pages=pages, _c=c, _ref=ctypes.byref(c))
 
 
 def alloc_kv_cache(fmt: int, pages: int, heads: int, dim: int, page_tokens: int = 64, block_tokens: int = 64,
@@ -416,10 +423,11 @@ def alloc_kv_cache(fmt: int, pages: int, heads: int, dim: int, page_tokens: int 
                    torch.empty(s, dtype=torch.float32, device=device))
 
 
-class KvBatch:
+class KvBatch(_Handle):
     """The sequences of a call: page_table [batch, max_pages], seq_lens [batch]
     and q_start [batch + 1] are int32 device tensors (q_start None: max_q rows
-    of every sequence); max_len bounds seq_lens (0: what the table holds)."""
+    of every sequence), whose contents may change between calls; max_len bounds
+    seq_lens (0: what the table holds)."""
 
     def __init__(self, page_table: torch.Tensor, seq_lens: torch.Tensor, q_start: Optional[torch.Tensor],
                  total_q: int, max_q: int, max_len: int = 0):
@@ -429,11 +437,10 @@ class KvBatch:
         batch, max_pages = page_table.shape
         if seq_lens.numel() != batch or (q_start is not None and q_start.numel() != batch + 1):
             raise ValueError("seq_lens has batch entries and q_start batch + 1")
-        self.page_table, self.seq_lens, self.q_start = page_table, seq_lens, q_start
-        self.total_q, self.max_q, self.max_len = total_q, max_q, max_len
-        self._c = FqKvBatch(batch, max_pages, max_q, max_len, total_q, page_table.data_ptr(), seq_lens.data_ptr(),
-                            None if q_start is None else q_start.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        c = FqKvBatch(batch, max_pages, max_q, max_len, total_q, page_table.data_ptr(), seq_lens.data_ptr(),
+                      None if q_start is None else q_start.data_ptr())
+        self.__dict__.update(page_table=page_table, seq_lens=seq_lens, q_start=q_start, total_q=total_q, max_q=max_q,
+                             max_len=max_len, _c=c, _ref=ctypes.byref(c))
 
 
 def _rows3(t: torch.Tensor, total: int, heads: int, dim: int, what: str) -> int:

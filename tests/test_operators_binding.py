@@ -75,3 +75,20 @@ def test_attention_leaves_the_descriptor_alone(monkeypatch):
     fq.fq_attention(cache(), batch(3), d, z(3, 4, 64, dtype=torch.bfloat16), z(3, 4, 64, dtype=torch.bfloat16), None, None,
                     Stream)
     assert seen[-1][-1] == 0 and d.q_stride == 1 << 30
+
+
+def test_handles_are_fixed():
+    """The library's structs are filled once: an attribute that could be set afterwards would say one thing and
+    the call do another, or leave the struct with a freed tensor's address."""
+    p = fq.Plane(z(4, 128, dtype=torch.uint8), z(4, 1))
+    c, b = cache(), batch(3, max_len=40)
+    for h, names in ((p, ("data", "scale")),
+                     (c, ("k", "v", "k_scale", "v_scale", "fmt", "block_tokens", "heads", "dim", "page_tokens", "pages")),
+                     (b, ("page_table", "seq_lens", "q_start", "total_q", "max_q", "max_len"))):
+        for name in names:
+            was = getattr(h, name)
+            for act in (lambda: setattr(h, name, 9), lambda: delattr(h, name)):
+                with pytest.raises(AttributeError):
+                    act()
+            assert getattr(h, name) is was
+    assert (b._c.max_len, b._c.total_q, b._c.max_q) == (b.max_len, b.total_q, b.max_q) == (40, 3, 1)
