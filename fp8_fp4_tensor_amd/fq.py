@@ -325,6 +325,24 @@ def fq_requantize_transpose(d: FqDesc, src: Quantized, dst: Quantized, stream=No
 
 
 # ---------------------------------------------------------------- operators on 8-bit data
+_ELSEWHERE = "the tensors of a call are on one GPU"
+
+
+def _one_gpu(on: int, *tensors: Optional[torch.Tensor]):
+    """Tensors that are given are on GPU `on` (-1: none): a host address would fault the GPU inside the kernel."""
+    if on < 0:
+        raise ValueError(_ELSEWHERE)
+    for t in tensors:
+        if t is not None and t.get_device() != on:
+            raise ValueError(_ELSEWHERE)
+
+
+def _common_gpu(*tensors: Optional[torch.Tensor]) -> int:
+    """The GPU that tensors share, -1 if there is none (the CPU: handles can be made there, calls cannot)."""
+    given = [t.get_device() for t in tensors if t is not None]
+    return given[0] if all(g == given[0] for g in given) else -1
+
+
 class _Handle:
     """A C struct with the tensors it points into. The struct is filled once, so
     the attributes are fixed: make another handle for other tensors or sizes."""
@@ -345,7 +363,8 @@ class Plane(_Handle):
         if data.element_size() != 1 or scale.dtype != torch.float32:
             raise TypeError("blockwise planes are 8-bit codes and float32 scales")
         c = FqPlane(data.data_ptr(), scale.data_ptr())
-        self.__dict__.update(data=data, scale=scale, _sizes=(data.numel(), scale.numel()), _c=c, _ref=ctypes.byref(c))
+        self.__dict__.update(data=data, scale=scale, _sizes=(data.numel(), scale.numel()), _on=_common_gpu(data, scale),
+                             _c=c, _ref=ctypes.byref(c))
 
     @classmethod
     def rowwise(cls, q: Quantized) -> "Plane":
@@ -373,7 +392,11 @@ def alloc_gemm_workspace(d: FqGemmDesc, device="cuda") -> Optional[torch.Tensor]
 
 
 def _nbytes(ws: Optional[torch.Tensor]) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("a workspace is contiguous")
+    return ws.numel() * ws.element_size()
 
 
 def fq_gemm(d: FqGemmDesc, a: Plane, b: Plane, out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
@@ -386,8 +409,10 @@ def fq_gemm(d: FqGemmDesc, a: Plane, b: Plane, out: torch.Tensor, ws: Optional[t
         raise ValueError("a scale for each block of 128 (and for 128 rows of b with b_block_rows 128)")
     if in_dtype_of(out) != d.out_dtype or not out.is_contiguous():
         raise TypeError("out is contiguous and of the descriptor's out_dtype")
+    size = _nbytes(ws)
+    _one_gpu(a._on if a._on == b._on else -1, out, ws)
     _check(lib().fq_gemm(ctypes.byref(d), a._ref, b._ref, out.data_ptr(),
-                         None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_gemm")
+                         None if ws is None else ws.data_ptr(), size, _stream(stream)), "fq_gemm")
 
 
 class KvCache(_Handle):
@@ -407,7 +432,8 @@ class KvCache(_Handle):
         c = FqKvCache(fmt, heads, dim, page, block_tokens, pages, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                       v_scale.data_ptr())
         self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, fmt=fmt, block_tokens=block_tokens, heads=heads,
-                             dim=dim, page_tokens=page, pages=pages, _c=c, _ref=ctypes.byref(c))
+                             dim=dim, page_tokens=page, pages=pages, _on=_common_gpu(k, v, k_scale, v_scale), _c=c,
+                             _ref=ctypes.byref(c))
 
 
 def alloc_kv_cache(fmt: int, pages: int, heads: int, dim: int, page_tokens: int = 64, block_tokens: int = 64,
@@ -440,7 +466,7 @@ class KvBatch(_Handle):
         c = FqKvBatch(batch, max_pages, max_q, max_len, total_q, page_table.data_ptr(), seq_lens.data_ptr(),
                       None if q_start is None else q_start.data_ptr())
         self.__dict__.update(page_table=page_table, seq_lens=seq_lens, q_start=q_start, total_q=total_q, max_q=max_q,
-                             max_len=max_len, _c=c, _ref=ctypes.byref(c))
+                             max_len=max_len, _on=_common_gpu(*given), _c=c, _ref=ctypes.byref(c))
 
 
 def _rows3(t: torch.Tensor, total: int, heads: int, dim: int, what: str) -> int:
@@ -464,6 +490,7 @@ def fq_kv_append(cache: KvCache, batch: KvBatch, k_new: torch.Tensor, v_new: tor
     dt = in_dtype_of(k_new)
     if v_new.dtype != k_new.dtype:
         raise TypeError("k_new and v_new have one dtype")
+    _one_gpu(cache._on if cache._on == batch._on else -1, k_new, v_new)
     _check(lib().fq_kv_append(cache._ref, batch._ref, dt, k_new.data_ptr(), ks,
                               v_new.data_ptr(), vs, _stream(stream)), "fq_kv_append")
 
@@ -501,6 +528,8 @@ def fq_attention(cache: KvCache, batch: KvBatch, d: FqAttentionDesc, q: torch.Te
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != batch.total_q * d.q_heads
                             or not lse.is_contiguous()):
         raise TypeError("lse is contiguous float32 [total_q, q_heads]")
+    size = _nbytes(ws)
+    _one_gpu(cache._on if cache._on == batch._on else -1, q, out, lse, ws)
     _check(lib().fq_attention(cache._ref, batch._ref, ctypes.byref(d), q.data_ptr(),
                               out.data_ptr(), None if lse is None else lse.data_ptr(),
-                              None if ws is None else ws.data_ptr(), _nbytes(ws), _stream(stream)), "fq_attention")
+                              None if ws is None else ws.data_ptr(), size, _stream(stream)), "fq_attention")

@@ -92,3 +92,63 @@ def test_handles_are_fixed():
                     act()
             assert getattr(h, name) is was
     assert (b._c.max_len, b._c.total_q, b._c.max_q) == (b.max_len, b.total_q, b.max_q) == (40, 3, 1)
+
+
+class Elsewhere(torch.Tensor):
+    """A CPU tensor that says it is on a GPU: what the checks before the launch see."""
+
+    @staticmethod
+    def on(t, index):
+        t = t.as_subclass(Elsewhere)
+        t.index = index
+        return t
+
+    def get_device(self):
+        return getattr(self, "index", -1)
+
+
+def test_tensors_off_the_gpu_are_refused(monkeypatch):
+    """A host address, or another GPU's, would fault the GPU inside the kernel. Every tensor of a call is asked."""
+    monkeypatch.setattr(fq, "lib", lambda: pytest.fail("the library was called"))
+
+    def refused(make, count):
+        """make(on): `on` places each of the call's tensors in turn. Tensor `odd` alone is elsewhere."""
+        for index in (-1, 1):
+            for odd in range(count):
+                at = iter(range(count))
+                with pytest.raises(ValueError, match="GPU"):
+                    make(lambda t: Elsewhere.on(t, index if next(at) == odd else 0))
+        with pytest.raises(ValueError, match="GPU"):
+            make(lambda t: t)
+
+    bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+
+    def product(on):
+        fq.fq_gemm(fq.gemm_desc(4, 128, 128), fq.Plane(on(z(4, 128, dtype=u8)), on(z(4, 1))),
+                   fq.Plane(on(z(128, 128, dtype=u8)), on(z(1, 1))), on(z(4, 128, dtype=bf)), on(z(64, dtype=u8)), Stream)
+
+    def handles(on):
+        c = fq.KvCache(0, 16, on(z(2, 2, 32, 64, dtype=u8)), on(z(2, 2, 64, 32, dtype=u8)), on(z(2, 2, 2)), on(z(2, 2, 2)))
+        return c, fq.KvBatch(on(z(3, 2, dtype=i32)), on(z(3, dtype=i32)), on(z(4, dtype=i32)), 3, 1)
+
+    def append(on):
+        fq.fq_kv_append(*handles(on), on(z(3, 2, 64)), on(z(3, 2, 64)), Stream)
+
+    def attend(on):
+        fq.fq_attention(*handles(on), fq.attention_desc(4), on(z(3, 4, 64, dtype=bf)), on(z(3, 4, 64, dtype=bf)),
+                        on(z(3, 4)), on(z(64, dtype=u8)), Stream)
+
+    refused(product, 6)
+    refused(append, 9)
+    refused(attend, 11)
+
+
+def test_workspaces_are_whole():
+    """A strided workspace's bytes are not where its size says."""
+    ws = z(4, 64, dtype=torch.uint8)[:, :16]
+    with pytest.raises(ValueError, match="workspace"):
+        fq.fq_gemm(fq.gemm_desc(4, 128, 128), fq.Plane(z(4, 128, dtype=torch.uint8), z(4, 1)),
+                   fq.Plane(z(128, 128, dtype=torch.uint8), z(1, 1)), z(4, 128, dtype=torch.bfloat16), ws, Stream)
+    with pytest.raises(ValueError, match="workspace"):
+        fq.fq_attention(cache(), batch(3), fq.attention_desc(4), z(3, 4, 64, dtype=torch.bfloat16),
+                        z(3, 4, 64, dtype=torch.bfloat16), None, ws, Stream)
