@@ -343,6 +343,16 @@ def _common_gpu(*tensors: Optional[torch.Tensor]) -> int:
     return given[0] if all(g == given[0] for g in given) else -1
 
 
+_FLOAT8 = {FQ_E4M3: torch.float8_e4m3fn, FQ_E5M2: torch.float8_e5m2}
+
+
+def _codes_of(fmt: int, *codes: torch.Tensor):
+    """Codes are bytes; a float8 type says what they are, and has to be the format's."""
+    for t in codes:
+        if t.element_size() != 1 or (t.is_floating_point() and t.dtype != _FLOAT8.get(fmt)):
+            raise TypeError("codes are 8-bit, and of the format where their type names one")
+
+
 class _Handle:
     """A C struct with the tensors it points into. The struct is filled once, so
     the attributes are fixed: make another handle for other tensors or sizes."""
@@ -360,7 +370,8 @@ class Plane(_Handle):
     def __init__(self, data: torch.Tensor, scale: torch.Tensor):
         if not (data.is_contiguous() and scale.is_contiguous()):
             raise ValueError("planes are contiguous")
-        if data.element_size() != 1 or scale.dtype != torch.float32:
+        _codes_of(FQ_E4M3, data)
+        if scale.dtype != torch.float32:
             raise TypeError("blockwise planes are 8-bit codes and float32 scales")
         c = FqPlane(data.data_ptr(), scale.data_ptr())
         self.__dict__.update(data=data, scale=scale, _sizes=(data.numel(), scale.numel()), _on=_common_gpu(data, scale),
@@ -425,7 +436,8 @@ class KvCache(_Handle):
             raise ValueError("k is [pages, heads, page_tokens, dim] and v is [pages, heads, dim, page_tokens]")
         if block_tokens < 1 or any(tuple(s.shape) != (pages, heads, page // block_tokens) for s in (k_scale, v_scale)):
             raise ValueError("scales are [pages, heads, page_tokens / block_tokens]")
-        if any(t.element_size() != 1 for t in (k, v)) or any(s.dtype != torch.float32 for s in (k_scale, v_scale)):
+        _codes_of(fmt, k, v)
+        if any(s.dtype != torch.float32 for s in (k_scale, v_scale)):
             raise TypeError("codes are 8-bit and scales float32")
         if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
             raise ValueError("cache buffers are contiguous")

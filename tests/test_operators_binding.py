@@ -152,3 +152,19 @@ def test_workspaces_are_whole():
     with pytest.raises(ValueError, match="workspace"):
         fq.fq_attention(cache(), batch(3), fq.attention_desc(4), z(3, 4, 64, dtype=torch.bfloat16),
                         z(3, 4, 64, dtype=torch.bfloat16), None, ws, Stream)
+
+
+def test_codes_of_another_format_are_refused():
+    """Bytes are taken as they are; a tensor that names its 8-bit format has to name the right one."""
+    e4, e5 = torch.float8_e4m3fn, torch.float8_e5m2
+    for ok in (torch.uint8, torch.int8, e4):
+        fq.Plane(z(4, 128, dtype=torch.uint8).view(ok), z(4, 1))
+    with pytest.raises(TypeError):
+        fq.Plane(z(4, 128, dtype=torch.uint8).view(e5), z(4, 1))
+    for fmt, right, wrong in ((fq.FQ_E4M3, e4, e5), (fq.FQ_E5M2, e5, e4)):
+        k, v, s = z(2, 2, 32, 64, dtype=torch.uint8), z(2, 2, 64, 32, dtype=torch.uint8), z(2, 2, 2)
+        fq.KvCache(fmt, 16, k, v, s, s)
+        fq.KvCache(fmt, 16, k.view(right), v.view(right), s, s)
+        for a, b in ((wrong, right), (right, wrong), (torch.uint8, wrong)):
+            with pytest.raises(TypeError):
+                fq.KvCache(fmt, 16, k.view(a), v.view(b), s, s)
