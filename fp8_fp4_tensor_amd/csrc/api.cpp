@@ -748,7 +748,7 @@ static fq_status kv_args(const fq_kv_cache* c, const fq_kv_batch* b, KvArgs& kv)
     kv.vs = c->v_scale;
     kv.batch = b->batch;
     kv.max_pages = b->max_pages;
-    kv.max_q = b->max_q;
+    kv.max_q = (int)(b->max_q < b->total_q ? b->max_q : b->total_q);  // rows of one sequence, whatever was declared
     const int64_t cap = (int64_t)b->max_pages * c->page_tokens;
     kv.max_len = c->num_pages == 0 ? 0 : (int)(b->max_len == 0 || b->max_len > cap ? cap : b->max_len);
     kv.total_q = b->total_q;
@@ -780,8 +780,6 @@ fq_status fq_kv_append(const fq_kv_cache* c, const fq_kv_batch* b, int32_t in_dt
     const int64_t row = (int64_t)kv.heads * kv.dim;
     if (k_stride < row || v_stride < row)
         return FQ_E_INVALID;
-    if ((int64_t)kv.batch * ((kv.max_q + kv.block - 2) / kv.block + 1) > 0x7fffffff)
-        return FQ_E_SHAPE;
     if (kv.batch == 0 || kv.max_q == 0 || kv.total_q == 0 || kv.max_len == 0)
         return FQ_OK;
     if (k_stride > kMaxElems / kv.total_q || v_stride > kMaxElems / kv.total_q)

@@ -47,21 +47,14 @@ __device__ __forceinline__ uint32_t move4(uint32_t c, float r)
 
 constexpr int kHold = 8;
 
+// The block of tokens [base, base + kv.block) of sequence `seq`, the first new
+// token of which is at position `first`.
 template <typename T, int FMT, bool IS_V>
-__device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, int64_t stride, int blocks_per_seq,
-                                             float* red)
+__device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, int64_t stride, int seq, int h,
+                                             const KvSeq& s, int first, int base, int tid, float* red)
 {
     constexpr int E = In<T>::kE;
-    const int seq = (int)(blockIdx.x / (unsigned)blocks_per_seq);
-    const int nth = (int)blockIdx.x - seq * blocks_per_seq;
-    const int h = blockIdx.y;
-    const KvSeq s = kv_seq(kv, seq);
-    const int first = s.len - s.nq;  // position of the first new token (below 0: it is not stored)
-    const int start = max(first, 0);
-    const int base = start / kv.block * kv.block + nth * kv.block;
-    const int lo = max(base, start), hi = min(base + kv.block, s.len);
-    if (lo >= hi)
-        return;
+    const int lo = max(base, first), hi = min(base + kv.block, s.len);  // (base is not negative)
     const int page = kv.table[(int64_t)seq * kv.max_pages + base / kv.page];
     const int dim = kv.dim, in_page = base & (kv.page - 1);
     const int at = lo - base, cnt = hi - lo;  // the new tokens of the block
@@ -76,12 +69,12 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
     const int loads = IS_V ? (int)cdiv(groups * per_row, kWG) * 4 : (int)cdiv(total, kWG);
     auto place = [&](int j, int& tok, int& d) {  // token of the block and first dim; false: none
         if constexpr (IS_V) {
-            const int u = (int)threadIdx.x + (j >> 2) * kWG, c = u / groups;
+            const int u = tid + (j >> 2) * kWG, c = u / groups;
             tok = (g0 + u - c * groups) * 4 + (j & 3);
             d = c * E;
             return c < per_row && tok >= at && tok < at + cnt;
         } else {
-            const int i = (int)threadIdx.x + j * kWG;
+            const int i = tid + j * kWG;
             tok = at + (i >> shift);
             d = (i & (per_row - 1)) * E;
             return i < total;
@@ -112,7 +105,7 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
     const float mine = __uint_as_float((uint32_t)(p + 127) << 23);
     const bool grows = at > 0 && mine > olds;
     const float sc = at > 0 && !grows ? olds : mine;
-    if (threadIdx.x == 0)
+    if (tid == 0)
         *scale = sc;
     // x / s: s is 2^p unless an older, larger scale stands
     const float inv = sc == mine ? __uint_as_float((uint32_t)(127 - p) << 23) : 1.0f / sc;
@@ -132,7 +125,7 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
         auto move16 = [&](u32x4 c) {
             return u32x4{move4<FMT>(c[0], r), move4<FMT>(c[1], r), move4<FMT>(c[2], r), move4<FMT>(c[3], r)};
         };
-        for (int i = threadIdx.x; i < n; i += 2 * kWG) {
+        for (int i = tid; i < n; i += 2 * kWG) {
             const bool two = i + kWG < n;
             uint8_t* c0 = place16(i);
             uint8_t* c1 = two ? place16(i + kWG) : c0;
@@ -144,7 +137,7 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
         if (IS_V && (at & 15)) {
             // whole words of four tokens, and by bytes the word that new tokens share
             const int from = at & ~15, words = (at - from + 3) >> 2;
-            for (int i = threadIdx.x; i < dim * words; i += kWG) {
+            for (int i = tid; i < dim * words; i += kWG) {
                 const int d = i / words, t = from + (i - d * words) * 4;
                 uint8_t* c = codes + (int64_t)d * kv.page + in_page + t;
                 if (t + 4 <= at) {
@@ -177,7 +170,7 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
             put(j, load(j));
     } else {
         auto put = [&](int j, u32x4 v0, u32x4 v1, u32x4 v2, u32x4 v3) {
-            const int u = (int)threadIdx.x + (j >> 2) * kWG, c = u / groups;
+            const int u = tid + (j >> 2) * kWG, c = u / groups;
             if (c >= per_row)
                 return;
             const int t = (g0 + u - c * groups) * 4;
@@ -210,21 +203,39 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
 
 template <typename T, int FMT>
 __global__ __launch_bounds__(kWG) void k_kv_append(KvArgs kv, const T* knew, int64_t kstride, const T* vnew,
-                                                   int64_t vstride, int blocks_per_seq)
+                                                   int64_t vstride)
 {
     __shared__ float red[4];
-    if (blockIdx.z == 0)
-        append_block<T, FMT, false>(kv, knew, kstride, blocks_per_seq, red);
-    else
-        append_block<T, FMT, true>(kv, vnew, vstride, blocks_per_seq, red);
+    const int seq = (int)blockIdx.y, is_v = (int)blockIdx.z >= kv.heads, h = (int)blockIdx.z - is_v * kv.heads;
+    const KvSeq s = kv_seq(kv, seq);
+    const int first = s.len - s.nq;  // position of the first new token (below 0: it is not stored)
+    const int start = max(first, 0);
+    if (start >= s.len)
+        return;
+    for (int base = start / kv.block * kv.block + (int)blockIdx.x * kv.block; base < s.len;
+         base += (int)gridDim.x * kv.block) {
+        // read anew in every turn: what follows from it would otherwise be kept
+        // over the loop, in 127 registers instead of 73
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        if (is_v)
+            append_block<T, FMT, true>(kv, vnew, vstride, seq, h, s, first, base, tid, red);
+        else
+            append_block<T, FMT, false>(kv, knew, kstride, seq, h, s, first, base, tid, red);
+    }
 }
 
+// Workgroups of a sequence and head: one for each block that max_q tokens can
+// touch, unless the sequences are of such different lengths that most of them
+// would find nothing. They are held to four times what total_q rows of equal
+// sequences would need, and take several blocks each.
 template <typename T, int FMT>
 hipError_t append(const KvArgs& kv, const void* k, int64_t ks, const void* v, int64_t vs, hipStream_t st)
 {
-    const int per = (kv.max_q + kv.block - 2) / kv.block + 1;  // blocks that max_q tokens can touch
-    const dim3 grid((unsigned)((int64_t)kv.batch * per), (unsigned)kv.heads, 2);
-    k_kv_append<T, FMT><<<grid, kWG, 0, st>>>(kv, (const T*)k, ks, (const T*)v, vs, per);
+    const int64_t per = (kv.max_q + kv.block - 2) / kv.block + 1;
+    const int64_t most = cdiv(4 * (cdiv(kv.total_q, kv.block) + 2 * (int64_t)kv.batch), kv.batch);
+    const dim3 grid((unsigned)(per < most ? per : most), (unsigned)kv.batch, (unsigned)kv.heads * 2);
+    k_kv_append<T, FMT><<<grid, kWG, 0, st>>>(kv, (const T*)k, ks, (const T*)v, vs);
     return hipGetLastError();
 }
 

@@ -1,0 +1,76 @@
+"""The 8-bit cache's operators where their ranges end: batches of very unequal
+sequences, bounds far above what they bound, extreme caps, scales and values."""
+import numpy as np
+import pytest
+import torch
+
+import operator_util as U
+import test_gpu_kv as K
+from fp8_fp4_tensor_amd import fq
+
+pytestmark = pytest.mark.gpu
+
+
+def empty_like(c: fq.KvCache) -> fq.KvCache:
+    return fq.KvCache(c.fmt, c.block_tokens, *(torch.zeros_like(t) for t in (c.k, c.v, c.k_scale, c.v_scale)))
+
+
+@pytest.mark.parametrize("batch,rows,heads,block", [(4096, 131072, 1, 16), (300, 5003, 3, 32), (65535, 70, 1, 128)])
+def test_append_of_one_prompt_among_single_tokens(batch, rows, heads, block):
+    """One call for all equals one call for the prompt and one for the single tokens. The first size has a block
+    of the longest sequence for each of 4096 sequences: 4096 * 8193 workgroups of 256 threads, were all launched."""
+    dim, page = 64, 256 if block < 128 else 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(batch)
+    per = -(-rows // page)
+    # the prompt's pages, then one page for each single token
+    table = torch.full((batch, per), -1, dtype=torch.int32, device="cuda")
+    at = batch // 3
+    order = torch.randperm(per + batch - 1, generator=g, device="cuda").to(torch.int32)
+    table[at] = order[:per]
+    others = torch.tensor([i for i in range(batch) if i != at], device="cuda")
+    table[others, 0] = order[per:]
+    lens = torch.ones(batch, dtype=torch.int32, device="cuda")
+    lens[at] = rows
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), lens.cumsum(0).to(torch.int32)])
+    k, v = (torch.randn((rows + batch - 1, heads, dim), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    whole = empty_like(fq.alloc_kv_cache(fq.FQ_E4M3, per + batch - 1, heads, dim, page, block))
+    apart = empty_like(whole)
+    fq.fq_kv_append(whole, fq.KvBatch(table, lens, starts, rows + batch - 1, rows), k, v)
+    torch.cuda.synchronize()
+    one = fq.KvBatch(table[at:at + 1].contiguous(), lens[at:at + 1].clone(), None, rows, rows)
+    fq.fq_kv_append(apart, one, k[at:at + rows], v[at:at + rows])
+    rest = torch.cat([torch.arange(at, device="cuda"), torch.arange(at + rows, rows + batch - 1, device="cuda")])
+    fq.fq_kv_append(apart, fq.KvBatch(table[others].contiguous(), lens[others].contiguous(), None, batch - 1, 1),
+                    k[rest], v[rest])
+    torch.cuda.synchronize()
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(whole, name), getattr(apart, name)), name
+
+
+def test_a_loose_bound_of_rows():
+    """max_q far above the rows: the same cache and the same attention."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    heads, q_heads, dim, page = 2, 4, 128, 64
+    lens, counts = [70, 3, 40], [5, 3, 9]
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(3, 2)
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    sd = torch.tensor(K.starts(counts), dtype=torch.int32, device="cuda")
+    k, v, q = (torch.randn((17, h, dim), generator=g, device="cuda").to(torch.bfloat16) for h in (heads, heads, q_heads))
+    first, outs = empty_like(fq.alloc_kv_cache(fq.FQ_E4M3, 6, heads, dim, page)), []
+    first.k_scale.fill_(2.0 ** -8)
+    first.v_scale.fill_(2.0 ** -8)
+    for max_q in (9, 1 << 24):
+        c = empty_like(first)
+        c.k_scale.copy_(first.k_scale)
+        c.v_scale.copy_(first.v_scale)
+        b, d = fq.KvBatch(table, ld, sd, 17, max_q), fq.attention_desc(q_heads)
+        fq.fq_kv_append(c, b, k, v)
+        out, lse = torch.empty_like(q), torch.empty((17, q_heads), device="cuda")
+        fq.fq_attention(c, b, d, q, out, lse, fq.alloc_attention_workspace(c, b, d))
+        torch.cuda.synchronize()
+        outs.append((c.k, c.v, c.k_scale, c.v_scale, out, lse))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.isfinite(outs[0][4].float()).all()
