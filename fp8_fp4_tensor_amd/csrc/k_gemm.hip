@@ -436,7 +436,7 @@ template <bool BF>
 __global__ __launch_bounds__(kWG) void k_gemm_join(GemmArgs g, int splits)
 {
     const int64_t total = g.m * g.n;
-    const int64_t e = ((int64_t)blockIdx.x * kWG + threadIdx.x) * 4;
+    const int64_t e = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWG + threadIdx.x) * 4;
     if (e >= total)
         return;
     if (total % 4) {  // partial results are not 16-byte aligned
@@ -463,7 +463,9 @@ __global__ __launch_bounds__(kWG) void k_gemm_join(GemmArgs g, int splits)
 
 hipError_t join(const GemmArgs& g, int splits, hipStream_t st)
 {
-    const unsigned blocks = (unsigned)cdiv(cdiv(g.m * g.n, 4), kWG);
+    // at most 2^26 workgroups; a grid's dimension has less than 2^32 threads
+    const int64_t need = cdiv(cdiv(g.m * g.n, 4), kWG), across = need < (1 << 23) ? need : 1 << 23;
+    const dim3 blocks((unsigned)across, (unsigned)cdiv(need, across));
     g.bf ? k_gemm_join<true><<<blocks, kWG, 0, st>>>(g, splits) : k_gemm_join<false><<<blocks, kWG, 0, st>>>(g, splits);
     return hipGetLastError();
 }
