@@ -815,7 +815,10 @@ static fq_status attention_args(const fq_kv_cache* c, const fq_kv_batch* b, cons
     a.q_heads = d->q_heads;
     a.window = d->window >= a.kv.max_len ? 0 : d->window;  // a window as long as any sequence hides nothing
     a.scale = d->scale != 0.0f ? d->scale : a.kv.dim == 64 ? 0.125f : a.kv.dim == 128 ? 0.08838834764831845f : 0.0625f;
-    a.softcap = d->softcap;
+    // both held to finite values: beyond them the cap does nothing, or leaves only zeros
+    const double cap2 = (double)d->softcap * 1.4426950408889634, most = 3.4028234663852886e38;
+    a.cap2 = (float)(cap2 < most ? cap2 : most);
+    a.cap_inv = cap2 > 0.0 ? (float)(1.0 / cap2 < most ? 1.0 / cap2 : most) : 0.0f;
     return FQ_OK;
 }
 

@@ -68,13 +68,29 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 rows, bf16x8 cols, f32x16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(rows, cols, c, 0, 0, 0);
 }
 
-// log2(e) cap * tanh(s / cap) = c2 (1 - 2 / (2^{x twice} + 1)): c2 = log2(e) cap,
-// and `twice` turns x into 2 log2(e) s / cap. The reciprocal is the
-// instruction's, off by a unit (an exact division made chunks of 2048 rows, 32
-// heads, up to 8192 keys 865 us; so 567).
-__device__ __forceinline__ float soft_cap(float x, float twice, float c2)
+// The cap: a score s (base 2) becomes c2 tanh(y), y = s / c2, c2 = log2(e) cap.
+// Near zero, for |y| <= 1/2, that is s times tanh(y) / y, a polynomial in y y
+// (equal-ripple fit of four terms, off by 1.4e-8, in fp32 by less than a unit), so
+// that the error is relative to the score however large the cap is. Further out
+// it is c2 (1 - 2 / (e^2y + 1)), where a unit of c2 is at most 2.2 units of the
+// result; the reciprocal is the instruction's, off by a unit. A wave whose scores
+// are all near, as they are under the usual caps, skips the exponential and the
+// reciprocal, 16 cycles each: 2 chunks of 2048 rows, 32 heads, up to 8192 keys take
+// 441 us without a cap, 559 with all scores near and 610 where most are far.
+constexpr float kCapNear = 0.5f;
+__device__ __forceinline__ float cap_ratio(float yy)
 {
-    return __builtin_fmaf(-2.0f * c2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * twice) + 1.0f), c2);
+    float p = 0.017256994f;
+    p = __builtin_fmaf(yy, p, -0.053052951f);
+    p = __builtin_fmaf(yy, p, 0.13325988f);
+    p = __builtin_fmaf(yy, p, -0.33333150f);
+    return __builtin_fmaf(yy, p, 1.0f);
+}
+__device__ __forceinline__ float soft_cap(float s, float c2, float inv)
+{
+    const float y = s * inv;
+    const float far = __builtin_fmaf(-2.0f * c2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y * (2.0f * kLog2e)) + 1.0f), c2);
+    return fabsf(y) <= kCapNear ? s * cap_ratio(y * y) : far;
 }
 
 // Max over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48), in every
@@ -184,8 +200,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
             q[c][1] = __builtin_bit_cast(bf16x8, ld16(p + c * 64 + 8));
         }
     }
-    // products to scores, base 2; with a cap to its tanh's argument
-    const float c2 = a.softcap * kLog2e, sc2 = a.scale * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
+    const float sc2 = a.scale * kLog2e;  // products to scores, base 2
     float m = -kInf, l = 0.0f;
     f32x4 o[T];
 #pragma unroll
@@ -239,14 +254,25 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
                 x[n * 4 + e] = d[e];
         }
         const float f = v.ks * sc2;
-        if (a.softcap > 0.0f) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[e] = soft_cap(x[e], f, c2);
-        } else {
+        for (int e = 0; e < 16; ++e)
+            x[e] *= f;
+        if (a.cap2 > 0.0f) {
+            float most = fabsf(x[0]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[e] *= f;
+            for (int e = 1; e < 16; ++e)
+                most = fmaxf(most, fabsf(x[e]));
+            if (__all(most * a.cap_inv <= kCapNear)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float y = x[e] * a.cap_inv;
+                    x[e] *= cap_ratio(y * y);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] = soft_cap(x[e], a.cap2, a.cap_inv);
+            }
         }
         const bool inside = t0 >= sp.lo && t0 + kStep <= end && v.ok && t0 + kStep - 1 <= pos && t0 >= oldest;
         if (!__all(inside)) {
@@ -447,8 +473,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         for (int k = 0; k < KK; ++k)
             q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 16) ^ u32x4{flip, flip, flip, flip});
     }
-    const float c2 = a.softcap * kLog2e;
-    const float sc2 = fabsf(a.scale) * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
+    const float sc2 = fabsf(a.scale) * kLog2e;  // products to scores, base 2
 
     float m = -kInf, l = 0.0f;
     f32x16 o[T];
@@ -579,13 +604,34 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         // anything: a hidden score is -inf times f)
         const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && (oks & 15) == 15 && t0 + kStep - 1 <= pos && t0 >= oldest;
         float f[2] = {kf[0], kf[1]};
-        if (a.softcap > 0.0f) {
+        if (a.cap2 > 0.0f) {
+            float most = 0.0f;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                f[n] = 1.0f;
+                float v = fabsf(x[n][0]);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[n][e] = soft_cap(x[n][e], kf[n], c2);
+                for (int e = 1; e < 16; ++e)
+                    v = fmaxf(v, fabsf(x[n][e]));
+                most = fmaxf(most, v * f[n]);
+            }
+            if (__all(most * a.cap_inv <= kCapNear)) {  // still products, and f their factor
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float g = fminf(f[n] * a.cap_inv, kFLT_MAX);  // finite, so that 0 stays 0
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float y = x[n][e] * g;
+                        x[n][e] *= cap_ratio(y * y);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[n][e] = soft_cap(x[n][e] * f[n], a.cap2, a.cap_inv);
+                    f[n] = 1.0f;
+                }
             }
         }
         if (!__all(inside)) {
@@ -654,7 +700,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         const int tv = t0 + mine;
         const float v = ok_next && tv < sp.hi && tv + 16 > sp.lo ? scale_next : 0.0f;
         const float k = scale_next * sc2;
-        return lane & 4 ? v : a.softcap > 0.0f ? k : fmaxf(k, 1e-30f);
+        return lane & 4 ? v : fmaxf(k, 1e-30f);
     };
 
     if (sp.from < sp.hi) {
@@ -747,8 +793,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
         for (int k = 0; k < KK; ++k)
             q[k] = __builtin_bit_cast(bf16x8, ld16(p + k * 32) ^ u32x4{flip, flip, flip, flip});
     }
-    const float c2 = a.softcap * kLog2e;
-    const float sc2 = fabsf(a.scale) * (a.softcap > 0.0f ? 2.0f * kLog2e / a.softcap : kLog2e);
+    const float sc2 = fabsf(a.scale) * kLog2e;  // products to scores, base 2
 
     float m = -kInf, l = 0.0f;
     f32x4 o[T];
@@ -849,12 +894,26 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
             for (int k = 0; k < KK; ++k)
                 x[n] = mfma(*(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn256(t)) * 8), q[k], x[n]);
         }
-        const float f = a.softcap > 0.0f ? 1.0f : fmaxf(ks * sc2, 1e-30f);
+        float f = fmaxf(ks * sc2, 1e-30f);
         const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok && t0 + kStep - 1 <= pos && t0 >= oldest;
-        if (a.softcap > 0.0f) {
+        if (a.cap2 > 0.0f) {  // as in k_attn_tile
+            float most = fabsf(x[0][0]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                x[e >> 2][e & 3] = soft_cap(x[e >> 2][e & 3], ks * sc2, c2);
+            for (int e = 1; e < 16; ++e)
+                most = fmaxf(most, fabsf(x[e >> 2][e & 3]));
+            if (__all(most * f * a.cap_inv <= kCapNear)) {
+                const float g = fminf(f * a.cap_inv, kFLT_MAX);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float y = x[e >> 2][e & 3] * g;
+                    x[e >> 2][e & 3] *= cap_ratio(y * y);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e >> 2][e & 3] = soft_cap(x[e >> 2][e & 3] * f, a.cap2, a.cap_inv);
+                f = 1.0f;
+            }
         }
         if (!__all(inside)) {
 #pragma unroll

@@ -250,7 +250,8 @@ hipError_t launch_kv_append(const KvArgs& kv, int in_bf16, const void* k_new, in
 struct AttnArgs {
     KvArgs kv;
     int q_heads = 0, window = 0;
-    float scale = 0.0f, softcap = 0.0f;
+    float scale = 0.0f;
+    float cap2 = 0.0f, cap_inv = 0.0f;  // the cap of the scores in base 2 (0: none) and its inverse
     const uint16_t* q = nullptr;     // [total_q, q_heads, dim] bf16, token stride q_stride
     int64_t q_stride = 0;
     uint16_t* out = nullptr;         // [total_q, q_heads, dim] bf16

@@ -542,6 +542,8 @@ fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32
  *   q_heads   a multiple of kv_heads; query head h reads kv head
  *             h / (q_heads / kv_heads)
  *   scale     0 selects 1 / sqrt(head_dim)
+ *   softcap   any finite value of at least 0; the capped score's error is
+ *             relative to the score, however large the cap
  *   q         [total_q, q_heads, head_dim] bf16, tokens q_stride elements apart
  *   out       [total_q, q_heads, head_dim] bf16, contiguous
  *   lse       [total_q, q_heads] fp32, or NULL

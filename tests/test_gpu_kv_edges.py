@@ -74,3 +74,62 @@ def test_a_loose_bound_of_rows():
     for a, b in zip(*outs):
         assert torch.equal(a, b)
     assert torch.isfinite(outs[0][4].float()).all()
+
+
+# ---------------------------------------------------------------- the cap
+# batch shapes that take each kernel: single tokens, whole and split; chunks of every head size
+KERNELS = {
+    "few-64": (1, 8, 64, [300, 41], [1, 1]), "few-128": (1, 4, 128, [300, 70], [1, 1]),
+    "few-128-split": (1, 4, 128, [2100, 70], [1, 1]), "few-256-split": (2, 4, 256, [1100], [3]),
+    "many-64": (32, 64, 64, [150, 128, 140, 200, 129, 300], [128] * 6), "many-128": (16, 64, 128, [520, 130], [515, 130]),
+    "many-256": (16, 32, 256, [300, 20], [300, 20]),
+}
+
+
+def capped_row(q, k, v, see, scale, cap):
+    """attention_row of operator_util with a cap's error relative to the score. tanh has a slope of at most 1, so
+    a score's own error does not grow. Below half the cap the result is the score times a polynomial: four fused
+    operations near 1, its fit (2^-26) and two products, under 4 units. Above it c2 (1 - 2 / (e + 1)): at most 2 c2
+    times the reciprocal's unit, c2 each for the exponential's unit, the sum and the last rounding, and y's two
+    roundings times y times tanh's slope, below c2 / 2 each: 6 units of c2, where c2 is at most 2.17 scores."""
+    dim = q.shape[0]
+    k, v = k[see], v[see]
+    s = k @ q * scale
+    eps = (dim + 4) * U.ULP32 * (np.abs(k) @ np.abs(q)).max() * abs(scale)
+    s = cap * np.tanh(s / cap)
+    eps += 14 * U.ULP32 * np.abs(s).max()
+    eps += 2 * 1.5 * np.abs(s).max() * 2 * U.ULP32 + 4 * U.ULP32
+    top = s.max()
+    p = np.exp(s - top)
+    z = p.sum()
+    o, w, lse = p @ v / z, p @ np.abs(v) / z, top + np.log(z)
+    sums = (int(see.sum()) / 16 + 64) * U.ULP32
+    bound = (U.HALF_BF16 + 2 * eps + 2 * sums) * w
+    return o, lse, bound + U.HALF_BF16 * (np.abs(o) + bound) + 1e-30, eps + sums + 4 * U.ULP32 * (abs(lse) + abs(top) + 1.0)
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 2.0, 12.0, 1e3, 1e4, 1e6, 1e9, 1e20, 3e38])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_caps_of_any_size(kernel, cap):
+    """From caps that leave nothing of the scores to caps that do nothing, with scores on both sides of half a cap."""
+    heads, q_heads, dim, lens, counts = KERNELS[kernel]
+    rng = np.random.default_rng(sorted(KERNELS).index(kernel))
+    page, group = 64, q_heads // heads
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, 0, heads, dim, page, 64, lens, table, pages, spread=3.0)
+    cap = float(np.float32(cap))
+    q, out, lse = K.attend(plain, table, lens, counts, q_heads, softcap=cap, rng=rng)
+    qs = K.starts(counts)
+    qd, od, ld = q.double().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    rows = [(i, j) for i in range(len(lens)) for j in range(0, counts[i], 97)]
+    for i, j in rows:
+        pos = lens[i] - counts[i] + j
+        for h in range(0, heads, max(1, heads // 2)):
+            k, v, there = plain.values(table[i], lens[i], h)
+            see = there & (np.arange(lens[i]) <= pos)
+            for u in (h * group, h * group + group - 1):
+                o, z, eo, ez = capped_row(qd[qs[i] + j, u], k, v, see, 1.0 / np.sqrt(dim), cap)
+                got, gz = od[qs[i] + j, u], ld[qs[i] + j, u]
+                assert np.all(np.abs(got - o) <= eo), (i, j, u, (np.abs(got - o) / eo).max())
+                assert abs(gz - z) <= ez, (i, j, u, gz, z, ez)
