@@ -38,6 +38,7 @@ constexpr int kMaxSplits = 1024;
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
+constexpr float kLeast = 0x1p-149f;  // the least factor of a score: -inf times it is -inf, the largest product times it 5e-7
 
 // Eight codes -> eight bf16 (exact).
 template <int FMT>
@@ -700,7 +701,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
         const int tv = t0 + mine;
         const float v = ok_next && tv < sp.hi && tv + 16 > sp.lo ? scale_next : 0.0f;
         const float k = scale_next * sc2;
-        return lane & 4 ? v : fmaxf(k, 1e-30f);
+        return lane & 4 ? v : fmaxf(k, kLeast);
     };
 
     if (sp.from < sp.hi) {
@@ -894,7 +895,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
             for (int k = 0; k < KK; ++k)
                 x[n] = mfma(*(const bf16x8*)(st.k + t * D + ((k * 4 + grp) ^ key_turn256(t)) * 8), q[k], x[n]);
         }
-        float f = fmaxf(ks * sc2, 1e-30f);
+        float f = fmaxf(ks * sc2, kLeast);
         const bool inside = t0 >= sp.lo && t0 + kStep <= sp.hi && ok && t0 + kStep - 1 <= pos && t0 >= oldest;
         if (a.cap2 > 0.0f) {  // as in k_attn_tile
             float most = fabsf(x[0][0]);

@@ -133,3 +133,24 @@ def test_caps_of_any_size(kernel, cap):
                 got, gz = od[qs[i] + j, u], ld[qs[i] + j, u]
                 assert np.all(np.abs(got - o) <= eo), (i, j, u, (np.abs(got - o) / eo).max())
                 assert abs(gz - z) <= ez, (i, j, u, gz, z, ez)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("zero_scales", [True, False], ids=["zero-scales", "tiny-scale"])
+def test_large_queries_meet_tiny_factors(kernel, zero_scales):
+    """Products near 1e33 times a factor that makes ordinary scores of them, or zeros: the factor is not held up."""
+    heads, q_heads, dim, lens, counts = KERNELS[kernel]
+    rng = np.random.default_rng(80)
+    page, group = 64, q_heads // heads
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, 0, heads, dim, page, 32, lens, table, pages)
+    q = K.bf16(rng, (sum(counts), q_heads, dim), 2.0 ** 100)
+    scale = 2.0 ** -100 / np.sqrt(dim)
+    if zero_scales:
+        plain.ks[np.isfinite(plain.ks)] = 0.0
+        scale = 1.0
+    scale = float(np.float32(scale))
+    q, out, lse = K.attend(plain, table, lens, counts, q_heads, scale=scale, q=q)
+    K.check_attention(plain, table, lens, counts, q_heads, q, out, lse, scale=scale,
+                      every=(61 if heads > 8 else 1))
