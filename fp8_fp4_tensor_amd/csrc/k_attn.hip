@@ -130,17 +130,19 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const KvSeq& s, int r
     return p;
 }
 
-// Four dims of an output row from its maximum (base 2), sum and accumulator.
+// Four dims of an output row from its maximum (base 2), sum and accumulator. The
+// sum is 0 for a row that sees nothing; a query that is no number gives a sum
+// that is none.
 __device__ __forceinline__ void finish(const AttnArgs& a, int64_t rid, int dim, int d, float top, float sum, f32x4 v)
 {
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint32_t b[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         b[e] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * inv));
     *(u32x2*)(a.out + rid * dim + d) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     if (a.lse && d == 0)
-        a.lse[rid] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : -kInf;
+        a.lse[rid] = sum == 0.0f ? -kInf : (top + __log2f(sum)) * kLn2;
 }
 
 // Few query rows (one token of a grouped head, or short runs): the waves of a

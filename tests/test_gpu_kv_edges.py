@@ -154,3 +154,25 @@ def test_large_queries_meet_tiny_factors(kernel, zero_scales):
     q, out, lse = K.attend(plain, table, lens, counts, q_heads, scale=scale, q=q)
     K.check_attention(plain, table, lens, counts, q_heads, q, out, lse, scale=scale,
                       every=(61 if heads > 8 else 1))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_query_that_is_no_number(kernel):
+    """Its row says so, in out and in lse (-inf would mean a row that sees nothing); the other rows are as without it."""
+    heads, q_heads, dim, lens, counts = KERNELS[kernel]
+    rng = np.random.default_rng(81)
+    page = 64
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, 0, heads, dim, page, 64, lens, table, pages)
+    q, out, lse = K.attend(plain, table, lens, counts, q_heads, rng=rng)
+    bad = q.clone()
+    at = [(0, 0), (sum(counts) - 1, q_heads - 1), (sum(counts) // 2, q_heads // 2)]
+    for (r, h), v in zip(at, (float("nan"), float("nan"), float("inf"))):
+        bad[r, h, 5] = v
+    _, got, gz = K.attend(plain, table, lens, counts, q_heads, q=bad)
+    hit = torch.zeros((sum(counts), q_heads), dtype=torch.bool, device="cuda")
+    for r, h in at:
+        hit[r, h] = True
+    assert torch.isnan(got[hit]).all() and torch.isnan(gz[hit]).all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(gz[~hit], lse[~hit])
