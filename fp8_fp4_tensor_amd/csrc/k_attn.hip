@@ -391,9 +391,11 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void k_attn(AttnArgs
         const int ro = r0 + orow;
         const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
         if constexpr (SPLIT) {
+            // accumulators first, in whole 16 bytes, then the maxima and sums
+            const int64_t at = rid * a.splits + split;
             if (d == 0)
-                *(float2*)(a.ws + (rid * a.splits + split) * 2) = make_float2(top, sum);
-            *(f32x4*)(a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + (rid * a.splits + split) * D + d) = v;
+                *(float2*)(a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * D + at * 2) = make_float2(top, sum);
+            *(f32x4*)(a.ws + at * D + d) = v;
         } else {
             finish(a, rid, D, d, top, sum, v);
         }
@@ -1014,8 +1016,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
     const Span sp = span_of(a, s, r0, min(r0 + kRows, rows), group);
     const int n = sp.hi > sp.from ? (int)cdiv(sp.hi - sp.from, a.chunk) : 0;
     const int64_t rid = (s.q0 + ro / group) * a.q_heads + h * group + ro % group;
-    const float2* ml = (const float2*)a.ws + rid * a.splits;
-    const float* from = a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * 2 + rid * a.splits * D;
+    const float* from = a.ws + rid * a.splits * D;
+    const float2* ml = (const float2*)(a.ws + kv.total_q * a.q_heads * (int64_t)a.splits * D) + rid * a.splits;
     const int w = threadIdx.x >> 6;
     float2 v[kMaxSplits / 256];
     float top = -kInf;

@@ -176,3 +176,56 @@ def test_a_query_that_is_no_number(kernel):
         hit[r, h] = True
     assert torch.isnan(got[hit]).all() and torch.isnan(gz[hit]).all()
     assert torch.equal(got[~hit], out[~hit]) and torch.equal(gz[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("dim,n,q_heads", [(128, 2700, 5), (64, 4700, 3), (256, 3100, 7)])
+def test_odd_numbers_of_partial_results(dim, n, q_heads):
+    """One row of an odd number of heads over an odd number of splits: accumulators are moved 16 bytes at a time,
+    wherever the maxima and sums beside them end. Nothing is written outside the reported workspace."""
+    rng = np.random.default_rng(82)
+    page = 64
+    pages = -(-n // page) + 2
+    table = K.tables(rng, [n], page, pages)
+    plain = K.filled(rng, 0, 1, dim, page, 64, [n], table, pages)
+    dev, b, d = K.to_device(plain), K.batch_of(table, [n], [1]), fq.attention_desc(q_heads)
+    size = fq.fq_attention_workspace(dev, b, d)
+    splits = size // (q_heads * (dim + 2) * 4)
+    assert size == splits * q_heads * (dim + 2) * 4 and (splits * q_heads) % 2 == 1 and splits > 1
+    q = K.bf16(rng, (1, q_heads, dim)).cuda()
+    pad = 4096
+    ws = torch.full((size + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((1, q_heads), device="cuda")
+    fq.fq_attention(dev, b, d, q, out, lse, ws[pad:pad + size])
+    torch.cuda.synchronize()
+    K.check_attention(plain, table, [n], [1], q_heads, q.cpu(), out, lse)
+    assert bool((ws[:pad] == 0xA5).all()) and bool((ws[pad + size:] == 0xA5).all())
+    # the accumulators are what the workspace begins with: finite 16-byte groups, then the pairs
+    acc = ws[pad:pad + splits * q_heads * dim * 4].view(torch.float32)
+    pairs = ws[pad + acc.numel() * 4:pad + size].view(torch.float32).view(q_heads, splits, 2)
+    assert torch.isfinite(acc).all() and bool((pairs[..., 1] > 0).all())
+    top = pairs[..., 0].amax(1, keepdim=True)
+    z = (pairs[..., 1] * torch.exp2(pairs[..., 0] - top)).sum(1)
+    assert torch.allclose(lse[0], (top[:, 0] + torch.log2(z)) * float(np.log(2.0)), rtol=0, atol=1e-4)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_writes_only_its_outputs(kernel):
+    """Guards around out and lse stay as they were, with rows that do not fill a tile."""
+    heads, q_heads, dim, lens, counts = KERNELS[kernel]
+    rng = np.random.default_rng(83)
+    page, n, pad = 64, sum(counts), 4096
+    pages = sum(-(-x // page) for x in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, 0, heads, dim, page, 64, lens, table, pages)
+    dev, b, d = K.to_device(plain), K.batch_of(table, lens, counts), fq.attention_desc(q_heads)
+    q = K.bf16(rng, (n, q_heads, dim)).cuda()
+    out = torch.full((n * q_heads * dim + 2 * pad,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n * q_heads + 2 * pad,), 7.0, device="cuda")
+    o, z = out[pad:-pad].view(n, q_heads, dim), lse[pad:-pad].view(n, q_heads)
+    o.fill_(float("nan"))
+    z.fill_(float("nan"))
+    fq.fq_attention(dev, b, d, q, o, z, fq.alloc_attention_workspace(dev, b, d))
+    torch.cuda.synchronize()
+    assert torch.isfinite(o.float()).all() and torch.isfinite(z).all()
+    for t in (out, lse):
+        assert bool((t[:pad] == 7.0).all()) and bool((t[-pad:] == 7.0).all())
