@@ -175,8 +175,11 @@ hipError_t few(const GemmArgs& g, hipStream_t st)
 // assembly because the compiler, which cannot tell the two stages apart,
 // would wait for every transfer before the next read of LDS; there is no
 // output register, and the waits are those of the step loop. M0 holds the
-// LDS address and needs one wait state before its use; nothing else here uses
-// it.
+// LDS address and needs one wait state before its use; naming it as written
+// keeps the compiler's own uses of it apart (it warns of any reserved register
+// in that list).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t to, int lane_offset, int offset)
 {
@@ -184,13 +187,14 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t to, in
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                      :
                      : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
-                     : "memory");
+                     : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                      :
                      : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
-                     : "memory");
+                     : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Workgroup -> tile. Workgroups go to the eight XCDs round robin and each XCD
 // has its own L2, so an XCD takes a run of consecutive tiles; runs walk down
