@@ -503,7 +503,9 @@ typedef struct {
  * the kernels hold every index to the declared sizes instead: lengths are cut
  * to max_len and the table's span, rows to total_q and max_q, and the
  * tokens of a page outside [0, num_pages) count as absent (not stored, not
- * seen). A page must belong to one sequence of a call.
+ * seen). A page that fq_kv_append writes to must belong to one sequence of the
+ * call; pages that are only read (a prefix that sequences share) may belong to
+ * any number.
  */
 typedef struct {
     int32_t batch;

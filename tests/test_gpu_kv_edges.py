@@ -229,3 +229,24 @@ def test_attention_writes_only_its_outputs(kernel):
     assert torch.isfinite(o.float()).all() and torch.isfinite(z).all()
     for t in (out, lse):
         assert bool((t[:pad] == 7.0).all()) and bool((t[-pad:] == 7.0).all())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_sequences_that_share_a_prefix(kernel):
+    """The same pages in several rows of the table: the same results as of copies of them."""
+    heads, q_heads, dim, lens, counts = KERNELS[kernel]
+    rng = np.random.default_rng(84)
+    page, batch = 64, max(2, len(lens))
+    n = max(lens)
+    lens, counts = [n - 3 * i for i in range(batch)], [min(max(counts), n - 3 * i) for i in range(batch)]
+    need = -(-n // page)
+    one = rng.permutation(need).astype(np.int32)
+    plain = K.filled(rng, 0, heads, dim, page, 64, [need * page], one[None], need)
+    q = K.bf16(rng, (sum(counts), q_heads, dim))
+    shared = np.repeat(one[None], batch, 0)
+    _, out, lse = K.attend(plain, shared, lens, counts, q_heads, q=q)
+    apart = U.PlainCache(0, need * batch, heads, dim, page, 64, rng)
+    for name in ("k", "v", "ks", "vs"):
+        getattr(apart, name)[...] = np.concatenate([getattr(plain, name)] * batch)
+    _, got, gz = K.attend(apart, shared + need * np.arange(batch, dtype=np.int32)[:, None], lens, counts, q_heads, q=q)
+    assert torch.equal(got, out) and torch.equal(gz, lse) and torch.isfinite(out.float()).all()
