@@ -23,6 +23,7 @@
 // joined over the four lane groups by two exchanges.
 #include "codec.hpp"
 #include "launch.hpp"
+#include "plan.hpp"
 
 namespace fq {
 namespace {
@@ -32,9 +33,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStep = 64;   // tokens a wave takes at once
-constexpr int kRows = 16;   // query rows of a workgroup
-constexpr int kMaxSplits = 1024;
+constexpr int kStep = kAttnStep;  // tokens a wave takes at once
+constexpr int kRows = kAttnRows;  // query rows of a workgroup
+constexpr int kMaxSplits = kAttnSplits;
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
@@ -436,14 +437,11 @@ struct KvStage {
     uint16_t k[kStep * D], v[D * kStep];
 };
 
-// Query rows of a workgroup, eight waves: 32 a wave, 16 with 256 dims.
-constexpr int tile_rows(int dim) { return dim == 256 ? 128 : 256; }
-
 template <int D, int FMT>
 __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
 {
     static_assert(D <= 128, "256 dims: k_attn_tile256");
-    constexpr int kTileRows = tile_rows(D), kWaveRows = 32, kThreads = 512;
+    constexpr int kTileRows = attn_tile_rows(D), kWaveRows = 32, kThreads = 512;
     constexpr int KK = D / 16, T = D / 32;
     constexpr int kLoads = 8 * D / kThreads;  // 16-byte chunks of codes a thread brings for a step
     __shared__ KvStage<D> stage[2];
@@ -764,7 +762,7 @@ __device__ __forceinline__ int key_turn256(int t) { return (t & 3) | (t >> 2 & 1
 template <int FMT>
 __global__ __launch_bounds__(512, 2) void k_attn_tile256(AttnArgs a)
 {
-    constexpr int D = 256, kTileRows = tile_rows(D), kWaveRows = 16;
+    constexpr int D = 256, kTileRows = attn_tile_rows(D), kWaveRows = 16;
     constexpr int KK = D / 32, T = D / 16;
     constexpr int kLoads = D / 64;  // 16-byte chunks of codes a thread brings for a step
     __shared__ KvStage<D> stage[2];
@@ -1099,52 +1097,13 @@ hipError_t by_format(const AttnArgs& a, hipStream_t st)
 size_t plan_attention(AttnArgs& a)
 {
     const KvArgs& kv = a.kv;
-    const int64_t group = a.q_heads / kv.heads;
-    // The kernel for many rows, where its workgroups fill the chip and their
-    // rows: a step of 64 keys costs it the same up to 256 workgroups, and the
-    // kernel for few rows in proportion to its tiles of 16 rows. They are even at
-    // the tiles below, measured with 32 heads over 8, many against few in us: 128
-    // dims, 8 sequences of 128 rows and up to 2000 keys (2048 tiles) 71 and 88; 6
-    // of them (1536) 70 and 67; 2 of 320 rows and 8192 keys (1280) 252 and 224;
-    // 2 of 400 rows and 2000 keys (1600) 69 and 81; 64 dims, 8 of 128 rows (2048)
-    // 57 and 42; 256 dims, 4 of 128 rows (1024) 86 and 123.
-    const int64_t even = kv.dim == 64 ? 2800 : kv.dim == 128 ? 1600 : 725;
-    const int64_t wide = tile_rows(kv.dim);
-    const int64_t few_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, kRows);
-    const int64_t many_tiles = kv.batch * kv.heads * cdiv(kv.max_q * group, wide);
-    a.rows = kRows;
-    if (cdiv(many_tiles, 256) * even < few_tiles) {
-        a.rows = (int)wide;
-        a.tiles = (int)cdiv(kv.max_q * group, wide);
-        a.chunk = kv.max_len;
-        a.splits = 1;
-        return 0;
-    }
-    a.tiles = (int)cdiv(kv.max_q * group, kRows);
-    const int64_t tiles = (int64_t)kv.batch * kv.heads * a.tiles;
-    int64_t span = kv.max_len;
-    if (a.window > 0 && span > (int64_t)a.window + kv.max_q + kStep)
-        span = (int64_t)a.window + kv.max_q + kStep;
-    // One workgroup per tile if the tiles alone fill the chip, else about two
-    // workgroups a CU, each with at least a step for each of its four waves
-    // (4 sequences of up to 131072: 16 splits 164 us, 32 177, 64 169, 128 171;
-    // 64 of up to 8192: one 119 us, two 131, eight 120). A short run of keys
-    // on few tiles stays whole, on eight waves: no second launch.
-    a.waves = 4;
-    int64_t splits = tiles >= 512 ? 1 : cdiv(512, tiles > 0 ? tiles : 1);
-    if (splits > 1 && span <= 1024 && kv.dim <= 128) {
-        a.waves = 8;
-        splits = 1;
-    }
-    if (span < 1)
-        span = 1;
-    splits = splits < kMaxSplits ? splits : kMaxSplits;
-    const int64_t chunk = cdiv(cdiv(span, splits), 4 * kStep) * (4 * kStep);
-    a.chunk = (int)chunk;
-    a.splits = (int)cdiv(span, chunk);
-    if (a.splits == 1)
-        return 0;
-    return (size_t)(kv.total_q * a.q_heads) * a.splits * (kv.dim + 2) * sizeof(float);
+    const AttnPlan p = plan_attention(kv.batch, kv.heads, a.q_heads, kv.dim, kv.max_q, kv.max_len, a.window);
+    a.rows = p.rows;
+    a.tiles = p.tiles;
+    a.waves = p.waves;
+    a.chunk = p.chunk;
+    a.splits = p.splits;
+    return p.splits > 1 ? (size_t)(kv.total_q * a.q_heads) * p.splits * (kv.dim + 2) * sizeof(float) : 0;
 }
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t st)

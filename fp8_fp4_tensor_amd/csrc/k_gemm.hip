@@ -26,6 +26,7 @@
 // (any assignment of the depth serves, the same for both operands).
 #include "codec.hpp"
 #include "launch.hpp"
+#include "plan.hpp"
 
 namespace fq {
 namespace {
@@ -499,102 +500,14 @@ hipError_t tiled(GemmArgs g, int splits, hipStream_t st)
     return e == hipSuccess ? join(g, splits, st) : e;
 }
 
-// Which tile, and over how many shares of k. Each tile's time for one step
-// (one block of k), in us, alone on its CU and with as many as fit, measured
-// on products from 64x2048x7168 to 8192x14336x4096 (bf16 output, and fp32
-// with its half-rate products); steps times rounds of workgroups and the
-// bytes at 5 TB/s, the longer and a quarter of the other, plus the join's
-// launch and traffic, rank the choices. Measured both ways, the tile chosen against the next:
-// 2048x4096x4096 128x128 44.6 us, 256x256 55.8; 3000x4096x4096 256x256 57.2,
-// 128x128 73.6; 512x4096x14336 128x128 in 4 shares 49.8, whole 105, 64x128 in
-// 2 shares 56.1; 16x7168x18432 32x64 in 4 shares 28.2, k_gemm_few 46.6.
-struct TileCost {
-    int tm, tn, per_cu;
-    double alone[2], full[2];  // [bf16, fp32 output]
-};
-constexpr TileCost kTiles[] = {
-    {256, 256, 1, {1.75, 3.60}, {1.75, 3.60}},
-    {128, 128, 2, {0.94, 1.35}, {1.40, 2.20}},
-    {64, 128, 2, {0.67, 0.90}, {1.25, 1.50}},
-    {64, 64, 3, {0.60, 0.73}, {1.10, 1.30}},
-    {32, 64, 4, {0.42, 0.55}, {1.10, 1.20}},
-};
-constexpr int kTileKinds = 5;
-
-struct GemmPlan {
-    int kind = -1;     // index of kTiles, -1: k_gemm_few
-    int splits = 1;
-    double us = 0.0;   // by the ranking
-    int64_t main = 0;  // leading rows that go to 256x256 tiles first, a multiple of 256
-};
-
-GemmPlan plan_part(const GemmArgs& g, int64_t m)
-{
-    GemmPlan best;
-    const int64_t nb = g.k >> 7;
-    // Few rows, at most a workgroup of k_gemm_few a CU and at most 7 blocks a
-    // wave: one launch and no LDS (1x4096x4096: 5.4 us, 32x64 tiles 7.7;
-    // 1x4096x7168 7.9 and 9.7; beyond it they cross: 1x4096x14336 13.6 and 13.3)
-    if ((m <= 16 && g.n <= 4096 && nb <= 56) || (m <= 16 && g.n <= 8192 && nb <= 16))
-        return best;
-    constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
-    const int prec = g.bf ? 0 : 1;
-    const double bytes = (double)(m + g.n) * g.k + (double)m * g.n * (g.bf ? 2 : 4);
-    for (int k = 0; k < kTileKinds; ++k) {
-        const TileCost& t = kTiles[k];
-        const int64_t tiles = cdiv(m, t.tm) * cdiv(g.n, t.tn);
-        for (int s : kSplits) {
-            if (s > 1 && (nb / s < 2 || tiles >= 1024 || (double)s * m * g.n * 4 > 128e6))
-                break;
-            const int64_t per_cu = cdiv(tiles * s, 256);  // workgroups of the busiest CU
-            const int64_t rounds = per_cu / t.per_cu, left = per_cu % t.per_cu;
-            const double one = t.alone[prec], all = t.full[prec];
-            double step = rounds * all;
-            if (left)
-                step += t.per_cu == 1 ? one : one + (all - one) * (left - 1) / (t.per_cu - 1);
-            const double work = cdiv(nb, s) * step, read = bytes / 5e6;
-            double us = work > read ? work + read / 4 : read + work / 4;  // overlapped, but not wholly
-            if (s > 1)
-                us += 3.0 + (double)s * m * g.n * 8 / 6e6;
-            if (best.kind < 0 || us < best.us) {
-                best.kind = k;
-                best.splits = s;
-                best.us = us;
-            }
-        }
-    }
-    return best;
-}
-
-// 256x256 tiles that do not come out in whole rounds of the chip leave most of
-// it idle in the last one: the rows beyond the whole rounds are then a product
-// of their own, with the tile and shares that suit it (14336x4096x8192, fp32:
-// 3.5 rounds as 3 and 128x128 tiles).
-GemmPlan plan_gemm(const GemmArgs& g)
-{
-    GemmPlan best = plan_part(g, g.m);
-    const int64_t across = cdiv(g.n, 256), whole = cdiv(g.m, 256) * across / 256;
-    if (best.kind != 0 || best.splits > 1 || whole < 1)
-        return best;
-    const int64_t main = whole * 256 / across * 256;  // rows of `whole` rounds
-    if (main == 0 || main >= g.m)
-        return best;
-    GemmPlan rest = plan_part(g, g.m - main);
-    rest.us += plan_part(g, main).us + 2.0;
-    if (rest.kind < 0 || rest.us >= best.us)
-        return best;
-    rest.main = main;
-    return rest;
-}
-
 hipError_t launch_plan(const GemmArgs& g, int kind, int splits, hipStream_t st)
 {
     switch (kind) {
-    case 0: return tiled<256, 256, 4, 2, 2>(g, splits, st);
-    case 1: return tiled<128, 128, 2, 2, 2>(g, splits, st);
-    case 2: return tiled<64, 128, 1, 4, 3>(g, splits, st);
-    case 3: return tiled<64, 64, 1, 4, 3>(g, splits, st);
-    case 4: return tiled<32, 64, 1, 4, 3>(g, splits, st);
+    case 0: return tiled<kTileCosts[0].tm, kTileCosts[0].tn, 4, 2, 2>(g, splits, st);
+    case 1: return tiled<kTileCosts[1].tm, kTileCosts[1].tn, 2, 2, 2>(g, splits, st);
+    case 2: return tiled<kTileCosts[2].tm, kTileCosts[2].tn, 1, 4, 3>(g, splits, st);
+    case 3: return tiled<kTileCosts[3].tm, kTileCosts[3].tn, 1, 4, 3>(g, splits, st);
+    case 4: return tiled<kTileCosts[4].tm, kTileCosts[4].tn, 1, 4, 3>(g, splits, st);
     default: return few(g, st);
     }
 }
@@ -605,7 +518,7 @@ size_t gemm_workspace(const GemmArgs& g)
 {
     if (g.k == 0)
         return 0;
-    const GemmPlan p = plan_gemm(g);
+    const GemmPlan p = plan_gemm(g.m, g.n, g.k, g.bf);
     return p.splits > 1 ? (size_t)p.splits * (g.m - p.main) * g.n * sizeof(float) : 0;
 }
 
@@ -613,7 +526,7 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t st)
 {
     if (g.k == 0)
         return join(g, 0, st);
-    const GemmPlan p = plan_gemm(g);
+    const GemmPlan p = plan_gemm(g.m, g.n, g.k, g.bf);
     if (p.main == 0)
         return launch_plan(g, p.kind, p.splits, st);
     GemmArgs top = g, rest = g;

@@ -250,3 +250,85 @@ def test_sequences_that_share_a_prefix(kernel):
         getattr(apart, name)[...] = np.concatenate([getattr(plain, name)] * batch)
     _, got, gz = K.attend(apart, shared + need * np.arange(batch, dtype=np.int32)[:, None], lens, counts, q_heads, q=q)
     assert torch.equal(got, out) and torch.equal(gz, lse) and torch.isfinite(out.float()).all()
+
+
+# ---------------------------------------------------------------- every kernel
+# heads, q_heads, dim, lens, counts, window, cap, page, format: calls that take the kernel for many rows
+MANY = {
+    "64-scales": (32, 64, 64, [150, 128, 140, 200, 129, 300], [128] * 6, 0, 0.0, 64, 0),
+    "64-e5m2-window": (32, 96, 64, [700, 400, 333, 85, 120, 90], [85, 80, 85, 85, 0, 84], 90, 0.0, 16, 1),
+    "64-cap": (32, 64, 64, [200] * 6, [128, 128, 127, 128, 1, 128], 0, 5.0, 256, 0),
+    "128-e5m2": (16, 64, 128, [530, 300, 90], [511, 300, 0], 0, 0.0, 16, 1),
+    "128-window-cap": (16, 64, 128, [700, 520, 130, 64], [600, 513, 130, 1], 130, 9.0, 128, 0),
+    "256": (16, 32, 256, [300, 420, 20], [300, 257, 20], 77, 12.0, 32, 0),
+    "256-e5m2": (16, 48, 256, [300, 211], [300, 200], 0, 0.0, 256, 1),
+}
+# format, heads, q_heads, dim, lens, counts: calls that take the kernel for few rows, whole on four and eight waves and split
+FEW = {f"{name}-{dim}-{'e5m2' if fmt else 'e4m3'}": (fmt, heads, heads * group, dim, lens, counts)
+       for dim in (64, 128, 256) for fmt in (0, 1)
+       for name, heads, group, lens, counts in (
+           ("whole", 16, 5, [70 + i for i in range(33)], [1] * 33), ("one", 2, 3, [900, 77], [2, 5]),
+           ("split", 2, 4, [2500, 1030, 300], [1, 3, 0]))}
+
+
+@pytest.mark.parametrize("name", MANY)
+def test_many_rows(name):
+    """Scales that are no powers of two, zeros among them, in every form of the kernel for many rows."""
+    heads, q_heads, dim, lens, counts, window, cap, page, fmt = MANY[name]
+    rng = np.random.default_rng(sorted(MANY).index(name))
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, fmt, heads, dim, page, min(page, 32), lens, table, pages, spread=2.0)
+    for scales in (plain.ks, plain.vs):
+        scales *= rng.uniform(0.4, 1.7, size=scales.shape).astype(np.float32)
+        scales[rng.random(scales.shape) < 0.1] = 0.0
+    q, out, lse = K.attend(plain, table, lens, counts, q_heads, window, cap, rng=rng)
+    K.check_attention(plain, table, lens, counts, q_heads, q, out, lse, window, cap, every=67)
+
+
+@pytest.mark.parametrize("name", FEW)
+def test_few_rows(name):
+    fmt, heads, q_heads, dim, lens, counts = FEW[name]
+    rng = np.random.default_rng(100 + sorted(FEW).index(name))
+    page = 64
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = K.tables(rng, lens, page, pages)
+    plain = K.filled(rng, fmt, heads, dim, page, 32, lens, table, pages, spread=2.0)
+    q, out, lse = K.attend(plain, table, lens, counts, q_heads, rng=rng)
+    K.check_attention(plain, table, lens, counts, q_heads, q, out, lse)
+
+
+# heads, q_heads, dim, tokens, rows, pages of 64 tokens: caches whose keys pass 2^32 bytes
+FAR = {"many-64": (8, 32, 64, 1600, 1500, 150000), "many-128": (8, 32, 128, 1200, 1000, 75000),
+       "many-256": (8, 32, 256, 800, 700, 37500), "few-64-split": (8, 32, 64, 2000, 1, 150000),
+       "few-256-split": (8, 32, 256, 2000, 1, 37500)}
+
+
+@pytest.mark.parametrize("name", FAR)
+def test_far_pages(name):
+    """A sequence on the last pages of a cache of 4.9 GB of keys equals the same one on a small cache's."""
+    heads, q_heads, dim, n, count, pages = FAR[name]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    page = 64
+    used = -(-n // page)
+    big, small = (fq.alloc_kv_cache(fq.FQ_E4M3, p, heads, dim, page, page) for p in (pages, used))
+    assert big.k.numel() > 1 << 32
+    for c in (big, small):
+        c.k[-used:], c.v[-used:] = 0x7F, 0x7F  # NaN codes wherever nothing is stored
+    k, v, q = (torch.randn((r, h, dim), generator=g, device="cuda").to(torch.bfloat16)
+               for r, h in ((n, heads), (n, heads), (count, q_heads)))
+    outs = []
+    for c, last in ((big, pages), (small, used)):
+        table = torch.arange(last - used, last, dtype=torch.int32, device="cuda")[None].contiguous()
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        fq.fq_kv_append(c, fq.KvBatch(table, lens, None, n, n), k, v)
+        b, d = fq.KvBatch(table, lens, None, count, count), fq.attention_desc(q_heads)
+        out, lse = torch.empty_like(q), torch.empty((count, q_heads), device="cuda")
+        fq.fq_attention(c, b, d, q, out, lse, fq.alloc_attention_workspace(c, b, d))
+        torch.cuda.synchronize()
+        outs.append((out, lse))
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(big, name)[-used:], getattr(small, name)), name
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.isfinite(outs[0][0].float()).all()
