@@ -39,7 +39,10 @@ constexpr int kMaxSplits = kAttnSplits;
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
-constexpr float kLeast = 0x1p-149f;  // the least factor of a score: -inf times it is -inf, the largest product times it 5e-7
+// The least factor of a score: -inf times it is -inf, and the largest product
+// times it 6e-5, a product of 1e33 2e-10. (2^-149 is an operand of four bytes
+// less, and the code so placed 1.4% slower with 256 dims: 534 us for 527.)
+constexpr float kLeast = 0x1p-142f;
 
 // Eight codes -> eight bf16 (exact).
 template <int FMT>
