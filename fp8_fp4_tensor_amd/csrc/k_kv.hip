@@ -107,8 +107,18 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
     const float sc = at > 0 && !grows ? olds : mine;
     if (tid == 0)
         *scale = sc;
-    // x / s: s is 2^p unless an older, larger scale stands
-    const float inv = sc == mine ? __uint_as_float((uint32_t)(127 - p) << 23) : 1.0f / sc;
+    // x / s as a product where s is a power of two, and a quotient where an older
+    // scale that is none stands: x times a rounded inverse misses ties
+    const bool whole = (__float_as_uint(sc) & 0x7fffffu) == 0;
+    const float inv = sc == mine ? __uint_as_float((uint32_t)(127 - p) << 23) : whole ? 1.0f / sc : 1.0f;
+    auto unpack = [&](u32x4 v, float* f) {
+        In<T>::unpack(v, f);
+        if (!whole) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] /= sc;
+        }
+    };
 
     if (grows) {  // the block's older tokens, [0, at), move to the new scale
         const float r = olds * inv;
@@ -155,7 +165,7 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
             if (!place(j, tok, d))
                 return;
             float f[E];
-            In<T>::unpack(v, f);
+            unpack(v, f);
             uint32_t* o = (uint32_t*)(codes + (int64_t)(in_page + tok) * dim + d);
             if constexpr (E == 8)
                 *(u32x2*)o = u32x2{enc4<FMT>(f[0], f[1], f[2], f[3], inv), enc4<FMT>(f[4], f[5], f[6], f[7], inv)};
@@ -176,10 +186,10 @@ __device__ __forceinline__ void append_block(const KvArgs& kv, const T* fresh, i
             const int t = (g0 + u - c * groups) * 4;
             const int from = max(at - t, 0), to = min(at + cnt - t, 4);
             float f0[E], f1[E], f2[E], f3[E];
-            In<T>::unpack(v0, f0);
-            In<T>::unpack(v1, f1);
-            In<T>::unpack(v2, f2);
-            In<T>::unpack(v3, f3);
+            unpack(v0, f0);
+            unpack(v1, f1);
+            unpack(v2, f2);
+            unpack(v3, f3);
             uint8_t* o = codes + (int64_t)(c * E) * kv.page + in_page + t;
 #pragma unroll
             for (int e = 0; e < E; ++e, o += kv.page) {

@@ -527,8 +527,9 @@ typedef struct {
  * tokens, s = the smallest power of two of at least 2^-126 with a <= Fmax * s;
  * if the block holds older tokens and their scale is larger, that one is
  * kept, and if it is smaller their codes are moved to the new one,
- * q' = Q(fp32(dec(q) * fp32(s_old / s))). New codes are Q(x / s), to nearest even.
- * Powers of two make the move exact but for results in the format's
+ * q' = Q(fp32(dec(q) * fp32(s_old / s))). New codes are Q(fp32(x / s)), to
+ * nearest even (a kept older scale need not be a power of two). Powers of two
+ * make the division and the move exact but for results in the format's
  * subnormals. Rows at negative positions are skipped.
  */
 fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32_t in_dtype, const void *k_new,

@@ -332,3 +332,30 @@ def test_far_pages(name):
         assert torch.equal(getattr(big, name)[-used:], getattr(small, name)), name
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     assert torch.isfinite(outs[0][0].float()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("fmt", [fq.FQ_E4M3, fq.FQ_E5M2], ids=["e4m3", "e5m2"])
+def test_append_beside_scales_that_are_no_powers_of_two(fmt, dtype):
+    """A block that something else began keeps its larger scale: new codes are x / s, also where x / s lies half way
+    between two codes (x times the rounded inverse then falls on either side)."""
+    rng = np.random.default_rng(85)
+    heads, dim, page, block = 2, 64, 16, 16
+    odd = [3.0, 5.0, 3.0 * 2.0 ** -9, 7.0 * 2.0 ** -4, 5.0 * 2.0 ** 20, 3.0 * 2.0 ** -100]
+    plain = U.PlainCache(fmt, len(odd), heads, dim, page, block, rng)
+    man = 3 if fmt == fq.FQ_E4M3 else 2
+    # half way between neighbours, over several binades and both signs
+    ties = np.array([(1 + (2 * i + 1) / 2.0 ** (man + 1)) * 2.0 ** e for e in range(-5, 6) for i in range(2 ** man)])
+    old, new = 5, 9
+    x = np.zeros((len(odd), new, heads, dim))
+    for i, s in enumerate(odd):
+        plain.k[i, :, :old] = U.encode(rng.standard_normal((heads, old, dim)), fmt)
+        plain.v[i, :, :, :old] = U.encode(rng.standard_normal((heads, dim, old)), fmt)
+        plain.ks[i], plain.vs[i] = s, s
+        x[i] = rng.choice(ties, size=(new, heads, dim)) * rng.choice([-1.0, 1.0], size=(new, heads, dim)) * s
+    t = torch.from_numpy(x.reshape(-1, heads, dim)).to(dtype)
+    assert np.array_equal(t.double().numpy(), x.reshape(-1, heads, dim))  # exact in either type
+    dev = K.to_device(plain)
+    table = np.arange(len(odd), dtype=np.int32)[:, None]
+    K.append(dev, plain, table, [old + new] * len(odd), [new] * len(odd), t, -t)
+    K.same(dev, plain, "beside older scales")
