@@ -13,13 +13,20 @@ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // ---------------------------------------------------------------- products
 // Which tile, and over how many shares of k. Each tile's time for one step
 // (one block of k), in us, alone on its CU and with as many as fit, measured
-// on products from 64x2048x7168 to 8192x14336x4096 (bf16 output, and fp32
-// with its half-rate products); steps times rounds of workgroups and the
-// bytes at 5 TB/s, the longer and a quarter of the other, plus the join's
-// launch and traffic, rank the choices. Measured both ways, the tile chosen against the next:
-// 2048x4096x4096 128x128 44.6 us, 256x256 55.8; 3000x4096x4096 256x256 57.2,
-// 128x128 73.6; 512x4096x14336 128x128 in 4 shares 49.8, whole 105, 64x128 in
-// 2 shares 56.1; 16x7168x18432 32x64 in 4 shares 28.2, k_gemm_few 46.6.
+// on products from 64x2048x7168 to 8192x14336x4096: bf16 output with 128x128
+// scales, and fp32 output with 1x128 scales, the weight gradient's, with its
+// half-rate products (256x256 tiles, by 4096x4096 outputs of depths 2048 and
+// 14336: 1.79 and 3.67; the other two ways around 2.29 and 3.23). Steps times
+// rounds of workgroups and the bytes at 5 TB/s, the longer and a quarter of
+// the other, plus the join's launch and traffic, rank the choices. Measured
+// both ways, what is chosen first (us):
+//   2048x4096x4096    128x128 48.2, 256x256 56.4
+//   3000x4096x4096    256x256 57.9, 128x128 78.0
+//   1003x7168x2048    128x128 26.9, 256x256 32.1, 64x128 34.6
+//   512x4096x14336    256x256 in 8 shares 57.0, 128x128 in 4 60.8, whole 131
+//   48x18432x7168     64x128 in 3 shares 36.9, whole 40.8, in 2 45.4
+//   16x7168x18432     32x64 in 6 shares 31.1, k_gemm_few 46.1
+// The ranking is not exact: 4 shares of the last would take 28.7.
 struct TileCost {
     int tm, tn, per_cu;
     double alone[2], full[2];  // [bf16, fp32 output]
@@ -45,8 +52,9 @@ inline GemmPlan plan_gemm_part(int64_t m, int64_t n, int64_t k, bool bf)
     GemmPlan best;
     const int64_t nb = k >> 7;
     // Few rows, at most a workgroup of k_gemm_few a CU and at most 7 blocks a
-    // wave: one launch and no LDS (1x4096x4096: 5.4 us, 32x64 tiles 7.7;
-    // 1x4096x7168 7.9 and 9.7; beyond it they cross: 1x4096x14336 13.6 and 13.3)
+    // wave: one launch and no LDS (1x4096x4096: 6.7 us, 32x64 tiles 8.9;
+    // 1x4096x7168 7.9 and 9.8; beyond it little is between them: 1x4096x14336
+    // 13.6, and 14.3 to 15.1 by shares)
     if ((m <= 16 && n <= 4096 && nb <= 56) || (m <= 16 && n <= 8192 && nb <= 16))
         return best;
     constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
@@ -81,7 +89,8 @@ inline GemmPlan plan_gemm_part(int64_t m, int64_t n, int64_t k, bool bf)
 // 256x256 tiles that do not come out in whole rounds of the chip leave most of
 // it idle in the last one: the rows beyond the whole rounds are then a product
 // of their own, with the tile and shares that suit it (14336x4096x8192, fp32:
-// 3.5 rounds as 3 and 128x128 tiles).
+// 3.5 rounds as 3 and 256x256 tiles in two shares 883 us, all on whole 256x256
+// tiles 914, on 128x128 992).
 inline GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool bf)
 {
     GemmPlan best = plan_gemm_part(m, n, k, bf);
@@ -123,17 +132,21 @@ inline AttnPlan plan_attention(int64_t batch, int64_t heads, int64_t q_heads, in
     const int64_t group = q_heads / heads;
     // The kernel for many rows, where its workgroups fill the chip and their
     // rows: a step of 64 keys costs it the same up to 256 workgroups, and the
-    // kernel for few rows in proportion to its tiles of 16 rows. They are even at
-    // the tiles below, measured with 32 heads over 8, many against few in us: 128
-    // dims, 8 sequences of 128 rows and up to 2000 keys (2048 tiles) 71 and 88; 6
-    // of them (1536) 70 and 67; 2 of 320 rows and 8192 keys (1280) 252 and 224;
-    // 2 of 400 rows and 2000 keys (1600) 69 and 81; 64 dims, 8 of 128 rows (2048)
-    // 57 and 42; 256 dims, 4 of 128 rows (1024) 86 and 123.
-    const int64_t even = dim == 64 ? 2800 : dim == 128 ? 1600 : 725;
+    // kernel for few rows in proportion to its tiles of 16 rows. Many against few
+    // in us, sequences of 256 or 512 rows (tokens times group) and up to 2000 keys:
+    //   64 dims    2560 tiles 56.3 and 58.4, 2816 56.5 and 62.6, 3072 56.2 and 66.9;
+    //              with a cap 2560 72.7 and 70.8, 2816 72.5 and 74.9
+    //   128 dims   1280 tiles 69.3 and 64.2, 1536 69.6 and 73.0, 1792 69.7 and 83.0;
+    //              with a cap 1536 85.7 and 78.0, 1792 85.9 and 89.8
+    //   256 dims   512 tiles 86.5 and 76.5, 640 86.9 and 102.7, 768 86.6 and 110;
+    //              with a cap 512 95.5 and 81.8, 768 95.6 and 117
+    // (groups of 1 and of 8 within 2% of groups of 4). The borders stand at or above
+    // what is even, for the kernel for few rows rounds its probabilities less.
+    const int64_t border = dim == 64 ? 2800 : dim == 128 ? 1600 : 725;
     const int64_t wide = attn_tile_rows(dim);
     const int64_t few_tiles = batch * heads * ceil_div(max_q * group, kAttnRows);
     const int64_t many_tiles = batch * heads * ceil_div(max_q * group, wide);
-    if (ceil_div(many_tiles, 256) * even < few_tiles) {
+    if (ceil_div(many_tiles, 256) * border < few_tiles) {
         p.rows = (int)wide;
         p.tiles = (int)ceil_div(max_q * group, wide);
         p.chunk = (int)max_len;

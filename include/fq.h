@@ -554,7 +554,9 @@ fq_status fq_kv_append(const fq_kv_cache *cache, const fq_kv_batch *batch, int32
  * scales that are not negative; what no row of the call sees (a page's unused end, pages that
  * a window has left behind) may hold anything. Scores, softmax and sums are
  * fp32; probabilities times V's scale are bf16 in the product with V (two
- * bf16 terms where the call has few rows).
+ * bf16 terms where the call has few rows). Probabilities are relative to a
+ * maximum that may lag by up to 2^8 until the last division, so 2^8 times the
+ * sum of |V| over the tokens that a row sees has to be finite in fp32.
  */
 typedef struct {
     int32_t q_heads;
