@@ -757,7 +757,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a)
 
 // The same for 256 dims, whose accumulators leave no room for 32 rows a wave
 // at two waves a SIMD: 16 rows a wave and 16x16 tiles (2 chunks of 2048 rows, 16
-// heads over 4, up to 8192 keys: 517 us; 32x32 tiles with one wave a SIMD 627).
+// heads over 4, up to 8192 keys: 527 us; 32x32 tiles with one wave a SIMD 627).
 // Score tiles as in k_attn, one block of 16 tokens a lane; tokens 16 g + 8 k
 // .. + 7 of a dim are chunk g + 4 k, so that a read meets no bank twice.
 __device__ __forceinline__ int key_turn256(int t) { return (t & 3) | (t >> 2 & 12); }

@@ -10,8 +10,8 @@
 // those.
 //
 // Bound by latency for single tokens (lengths, then page and rows, then the
-// codes) and by memory for prompts. One workgroup takes one block of one head,
-// K or V, and holds its rows in registers between the amax and the cast (a
+// codes) and by memory for prompts. One workgroup takes one block of one head
+// (several where sequences are very unequal), K or V, and holds its rows in registers between the amax and the cast (a
 // block of up to 8 16-byte loads a thread: 64 tokens of 128 bf16 dims take 4;
 // larger ones are read again, from cache). The cache holds V transposed
 // (k_attn.hip says why): a thread takes four tokens of the same dims, and the
