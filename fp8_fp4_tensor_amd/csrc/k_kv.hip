@@ -11,12 +11,12 @@
 //
 // Bound by latency for single tokens (lengths, then page and rows, then the
 // codes) and by memory for prompts. One workgroup takes one block of one head
-// (several where sequences are very unequal), K or V, and holds its rows in registers between the amax and the cast (a
-// block of up to 8 16-byte loads a thread: 64 tokens of 128 bf16 dims take 4;
-// larger ones are read again, from cache). The cache holds V transposed
-// (k_attn.hip says why): a thread takes four tokens of the same dims, and the
-// converter packs them token by token, so the transposed code words come out
-// of registers with no exchange.
+// (several where sequences are very unequal), K or V, and holds its rows in
+// registers between the amax and the cast (a block of up to 8 16-byte loads a
+// thread: 64 tokens of 128 bf16 dims take 4; larger ones are read again, from
+// cache). The cache holds V transposed (k_attn.hip says why): a thread takes
+// four tokens of the same dims, and the converter packs them token by token, so
+// the transposed code words come out of registers with no exchange.
 #include "codec.hpp"
 #include "launch.hpp"
 
