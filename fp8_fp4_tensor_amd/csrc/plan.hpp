@@ -134,7 +134,7 @@ inline AttnPlan plan_attention(int64_t batch, int64_t heads, int64_t q_heads, in
     // rows: a step of 64 keys costs it the same up to 256 workgroups, and the
     // kernel for few rows in proportion to its tiles of 16 rows. Many against few
     // in us, sequences of 256 or 512 rows (tokens times group) and up to 2000 keys:
-    //   64 dims    2560 tiles 56.3 and 58.4, 2816 56.5 and 62.6, 3072 56.2 and 66.9;
+    //   64 dims    2048 tiles 56.4 and 49.9, 2560 56.3 and 58.4, 2816 56.5 and 62.6;
     //              with a cap 2560 72.7 and 70.8, 2816 72.5 and 74.9
     //   128 dims   1280 tiles 69.3 and 64.2, 1536 69.6 and 73.0, 1792 69.7 and 83.0;
     //              with a cap 1536 85.7 and 78.0, 1792 85.9 and 89.8
