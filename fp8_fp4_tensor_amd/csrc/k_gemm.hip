@@ -26,13 +26,11 @@
 // (any assignment of the depth serves, the same for both operands).
 #include "codec.hpp"
 #include "launch.hpp"
+#include "matrix.hpp"
 #include "plan.hpp"
 
 namespace fq {
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -61,48 +59,6 @@ __device__ __forceinline__ f32x4 mfma_block(i32x8 rows, i32x8 cols)
         return c;
     }
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rows, cols, z, 0, 0, 0, 0, 0, 0);
-}
-
-__device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
-{
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-
-__device__ __forceinline__ uint32_t bf16_bits(float v)
-{
-    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
-// Four consecutive outputs C[i, j .. j+3] of a row; those at or past n are not written.
-template <bool BF>
-__device__ __forceinline__ void store4(void* c, int64_t i, int64_t j, int64_t n, f32x4 v, bool acc)
-{
-    if constexpr (BF) {
-        uint16_t* p = (uint16_t*)c + i * n + j;
-        if ((n & 3) == 0) {
-            if (j < n)
-                *(u32x2*)p = u32x2{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < n)
-                p[e] = (uint16_t)bf16_bits(v[e]);
-    } else {
-        float* p = (float*)c + i * n + j;
-        if ((n & 3) == 0) {
-            if (j < n) {
-                if (acc)
-                    v += *(const f32x4*)p;
-                *(f32x4*)p = v;
-            }
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < n)
-                p[e] = acc ? p[e] + v[e] : v[e];
-    }
 }
 
 // Few rows of A (m <= 16) and no more columns than the chip holds at once: one
@@ -172,47 +128,6 @@ hipError_t few(const GemmArgs& g, hipStream_t st)
 // twice; the transfer writes LDS in lane order, so it is the lane's source
 // address that carries the permutation.
 
-// 64 lanes' 16 (or 4) bytes each -> LDS at `to`, in lane order. Written as
-// assembly because the compiler, which cannot tell the two stages apart,
-// would wait for every transfer before the next read of LDS; there is no
-// output register, and the waits are those of the step loop. M0 holds the
-// LDS address and needs one wait state before its use; naming it as written
-// keeps the compiler's own uses of it apart (it warns of any reserved register
-// in that list).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int BYTES>
-__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t to, int lane_offset, int offset)
-{
-    if constexpr (BYTES == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     :
-                     : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
-                     : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                     :
-                     : "s"(to), "v"(lane_offset), "s"(r), "s"(offset)
-                     : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// Workgroup -> tile. Workgroups go to the eight XCDs round robin and each XCD
-// has its own L2, so an XCD takes a run of consecutive tiles; runs walk down
-// groups of eight tile rows, so the ~32 tiles an XCD works on at once share
-// their rows of A and of B.
-__device__ __forceinline__ void tile_of(const GemmArgs& g, int64_t& tm, int64_t& tn)
-{
-    const uint32_t total = gridDim.x, per = total / 8, rest = total % 8;
-    const uint32_t xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
-    const uint32_t t = xcd * per + min(xcd, rest) + nth;
-    const uint32_t wide = 8 * (uint32_t)g.tiles_n;
-    const uint32_t band = t / wide, in = t - band * wide;
-    const uint32_t high = min(8u, (uint32_t)g.tiles_m - band * 8);
-    tn = in / high;
-    tm = band * 8 + (in - (uint32_t)tn * high);
-}
-
 template <int TM, int TN, int WM, int WN, int NS, bool B1>
 struct Tile {
     static constexpr int kNW = WM * WN;
@@ -241,7 +156,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_tile(GemmArgs g)
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, grp = lane >> 4;
     int64_t tm, tn;
-    tile_of(g, tm, tn);
+    tile_of(g.tiles_m, g.tiles_n, tm, tn);
     const int64_t m0 = tm * TM, n0 = tn * TN;
     const int nb = (int)(g.k >> 7);
     // this workgroup's blocks of k: [first, last)
@@ -466,7 +381,9 @@ __global__ __launch_bounds__(kWG) void k_gemm_join(GemmArgs g, int splits)
     store4<BF>(g.c, 0, e, total, v, g.acc);
 }
 
-hipError_t join(const GemmArgs& g, int splits, hipStream_t st)
+}  // namespace
+
+hipError_t launch_gemm_join(const GemmArgs& g, int splits, hipStream_t st)
 {
     // at most 2^26 workgroups; a grid's dimension has less than 2^32 threads
     const int64_t need = cdiv(cdiv(g.m * g.n, 4), kWG), across = need < (1 << 23) ? need : 1 << 23;
@@ -474,6 +391,8 @@ hipError_t join(const GemmArgs& g, int splits, hipStream_t st)
     g.bf ? k_gemm_join<true><<<blocks, kWG, 0, st>>>(g, splits) : k_gemm_join<false><<<blocks, kWG, 0, st>>>(g, splits);
     return hipGetLastError();
 }
+
+namespace {
 
 template <int TM, int TN, int WM, int WN, int NS, bool SPLIT>
 hipError_t run_tiles(const GemmArgs& g, int splits, hipStream_t st)
@@ -497,7 +416,7 @@ hipError_t tiled(GemmArgs g, int splits, hipStream_t st)
     if (splits <= 1)
         return run_tiles<TM, TN, WM, WN, NS, false>(g, 1, st);
     const hipError_t e = run_tiles<TM, TN, WM, WN, NS, true>(g, splits, st);
-    return e == hipSuccess ? join(g, splits, st) : e;
+    return e == hipSuccess ? launch_gemm_join(g, splits, st) : e;
 }
 
 hipError_t launch_plan(const GemmArgs& g, int kind, int splits, hipStream_t st)
@@ -525,7 +444,7 @@ size_t gemm_workspace(const GemmArgs& g)
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st)
 {
     if (g.k == 0)
-        return join(g, 0, st);
+        return launch_gemm_join(g, 0, st);
     const GemmPlan p = plan_gemm(g.m, g.n, g.k, g.bf);
     if (p.main == 0)
         return launch_plan(g, p.kind, p.splits, st);
