@@ -288,6 +288,55 @@ void record_tag(int64_t t, int64_t H, uint32_t tag[2])
 
 float fmax_of(const fq_desc* d) { return d->format == FQ_E4M3 ? 448.0f : 57344.0f; }
 
+// The planes that an operator quantizes its [rows, cols] result to: their
+// descriptor, their buffers and the kernels' name for the recipe.
+fq_status check_planes(const fq_desc* planes, const fq_quantized* out, int64_t rows, int64_t cols, int& kind)
+{
+    fq_desc d = *planes;
+    d.in_dtype = FQ_IN_F32;  // not read
+    fq_status s = check_desc(&d);
+    if (s != FQ_OK)
+        return s;
+    if (d.rows != rows || d.cols != cols)
+        return FQ_E_SHAPE;
+    if (d.rounding != FQ_ROUND_NEAREST_EVEN || d.transform != FQ_TRANSFORM_NONE)
+        return FQ_E_UNSUPPORTED;
+    if (d.recipe == FQ_MX)
+        kind = d.format == FQ_E4M3 ? kMxE4M3 : d.format == FQ_E5M2 ? kMxE5M2 : kMxE2M1;
+    else if (d.recipe == FQ_BLOCK_FP32 && d.block_rows == 1)
+        kind = d.scale_mode == FQ_SCALE_POW2 ? kBlockPow2 : kBlockFp32;
+    else
+        return FQ_E_UNSUPPORTED;
+    return check_out(&d, out, false);
+}
+
+template <typename Args>
+void set_planes(Args& a, const fq_desc* planes, const fq_quantized* out)
+{
+    if (planes->outputs & FQ_ROWWISE) {
+        a.q = (uint8_t*)out->rowwise.data;
+        a.s = out->rowwise.scale;
+    }
+    if (planes->outputs & FQ_COLWISE) {
+        a.qt = (uint8_t*)out->colwise.data;
+        a.st = out->colwise.scale;
+    }
+}
+
+bool in_dtype(int32_t t) { return t == FQ_IN_F32 || t == FQ_IN_BF16; }
+
+// A row stride (0: contiguous) that keeps rows 16-byte aligned and apart.
+fq_status check_stride(int64_t& stride, int64_t cols, int64_t rows, int32_t dtype)
+{
+    if (stride == 0)
+        stride = cols;
+    if (stride < cols)
+        return FQ_E_INVALID;
+    if (rows > 0 && stride > kMaxElems / rows)
+        return FQ_E_SHAPE;
+    return stride % (dtype == FQ_IN_BF16 ? 8 : 4) ? FQ_E_ALIGN : FQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -860,6 +909,253 @@ fq_status fq_attention(const fq_kv_cache* c, const fq_kv_batch* b, const fq_atte
     a.lse = lse;
     a.ws = (float*)ws;
     return hip_status(launch_attention(a, st));
+}
+
+// ---------------------------------------------------------------- a feed-forward block on microscaled data
+static fq_status check_gemm_mx(const fq_gemm_mx_desc* d)
+{
+    if (!d || d->m < 0 || d->n < 0 || d->k < 0)
+        return FQ_E_INVALID;
+    if (d->a_format < FQ_E4M3 || d->a_format > FQ_E2M1 || d->b_format < FQ_E4M3 || d->b_format > FQ_E2M1)
+        return FQ_E_INVALID;
+    if (d->out_dtype != FQ_IN_F32 && d->out_dtype != FQ_IN_BF16)
+        return FQ_E_INVALID;
+    if (d->accumulate != 0 && d->accumulate != 1)
+        return FQ_E_INVALID;
+    if (d->accumulate && d->out_dtype != FQ_IN_F32)
+        return FQ_E_UNSUPPORTED;
+    if (d->k % 32 || d->k > (int64_t(1) << 22))
+        return FQ_E_SHAPE;
+    auto over = [](int64_t x, int64_t y) { return y > 0 && x > kMaxElems / y; };
+    if (over(d->m, d->k) || over(d->n, d->k) || over(d->m, d->n))
+        return FQ_E_SHAPE;
+    return FQ_OK;
+}
+
+static GemmMxArgs gemm_mx_args(const fq_gemm_mx_desc* d)
+{
+    GemmMxArgs g;
+    g.m = d->m;
+    g.n = d->n;
+    g.k = d->k;
+    g.fa = d->a_format;
+    g.fb = d->b_format;
+    g.bf = d->out_dtype == FQ_IN_BF16;
+    g.acc = d->accumulate;
+    return g;
+}
+
+fq_status fq_gemm_mx_workspace(const fq_gemm_mx_desc* d, size_t* bytes)
+{
+    const fq_status s = check_gemm_mx(d);
+    if (s != FQ_OK)
+        return s;
+    if (bytes)
+        *bytes = d->m == 0 || d->n == 0 ? 0 : gemm_mx_workspace(gemm_mx_args(d));
+    return FQ_OK;
+}
+
+fq_status fq_gemm_mx(const fq_gemm_mx_desc* d, const fq_plane* a, const fq_plane* b, void* out, void* ws,
+                     size_t ws_bytes, hipStream_t st)
+{
+    const fq_status s = check_gemm_mx(d);
+    if (s != FQ_OK)
+        return s;
+    if (!a || !b)
+        return FQ_E_INVALID;
+    if (d->m == 0 || d->n == 0)
+        return FQ_OK;
+    if (!out || (d->k > 0 && (!a->data || !a->scale || !b->data || !b->scale)))
+        return FQ_E_INVALID;
+    if (!aligned(out, 16) || !aligned(a->data, 16) || !aligned(a->scale, 16) || !aligned(b->data, 16) ||
+        !aligned(b->scale, 16))
+        return FQ_E_ALIGN;
+    GemmMxArgs g = gemm_mx_args(d);
+    const size_t need = gemm_mx_workspace(g);
+    if (need) {
+        if (!ws || ws_bytes < need)
+            return FQ_E_WORKSPACE;
+        if (!aligned(ws, 16))
+            return FQ_E_ALIGN;
+    }
+    g.a = (const uint8_t*)a->data;
+    g.sa = (const uint8_t*)a->scale;
+    g.b = (const uint8_t*)b->data;
+    g.sb = (const uint8_t*)b->scale;
+    g.c = out;
+    g.ws = (uint8_t*)ws;
+    return hip_status(launch_gemm_mx(g, st));
+}
+
+static fq_status check_rmsnorm(const fq_rmsnorm_desc* d)
+{
+    if (!d || d->rows < 0 || d->cols < 0)
+        return FQ_E_INVALID;
+    if (!in_dtype(d->x_dtype) || !in_dtype(d->h_dtype) || !in_dtype(d->weight_dtype) || !in_dtype(d->y_dtype))
+        return FQ_E_INVALID;
+    if (d->accumulate != 0 && d->accumulate != 1)
+        return FQ_E_INVALID;
+    if (!(d->eps > 0.0f) || !(d->eps - d->eps == 0.0f))
+        return FQ_E_INVALID;
+    if (d->cols % 8 || d->cols > 32768 || (d->cols > 0 && d->rows > kMaxElems / d->cols))
+        return FQ_E_SHAPE;
+    return FQ_OK;
+}
+
+fq_status fq_rmsnorm(const fq_rmsnorm_desc* d, const fq_desc* planes, const void* x, const void* residual,
+                     const void* weight, void* h, float* rstd, void* y, const fq_quantized* out, hipStream_t st)
+{
+    fq_status s = check_rmsnorm(d);
+    if (s != FQ_OK)
+        return s;
+    NormArgs a;
+    a.x_stride = d->x_stride;
+    if ((s = check_stride(a.x_stride, d->cols, d->rows, d->x_dtype)) != FQ_OK)
+        return s;
+    if (planes && (s = check_planes(planes, out, d->rows, d->cols, a.kind)) != FQ_OK)
+        return s;
+    if (d->rows == 0 || d->cols == 0)
+        return FQ_OK;
+    if ((!planes && !y) || !residual != !h || (planes && (planes->outputs & FQ_COLWISE) && !rstd))
+        return FQ_E_INVALID;
+    if (!x || !weight)
+        return FQ_E_INVALID;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(rstd, 4) ||
+        !aligned(y, 16))
+        return FQ_E_ALIGN;
+    a.rows = d->rows;
+    a.cols = d->cols;
+    a.x = x;
+    a.res = residual;
+    a.w = weight;
+    a.h = h;
+    a.rstd = rstd;
+    a.y = y;
+    a.x_bf = d->x_dtype == FQ_IN_BF16;
+    a.h_bf = d->h_dtype == FQ_IN_BF16;
+    a.w_bf = d->weight_dtype == FQ_IN_BF16;
+    a.y_bf = d->y_dtype == FQ_IN_BF16;
+    a.eps = d->eps;
+    if (planes)
+        set_planes(a, planes, out);
+    return hip_status(launch_rmsnorm(a, st));
+}
+
+fq_status fq_rmsnorm_workspace(const fq_rmsnorm_desc* d, size_t* bytes)
+{
+    const fq_status s = check_rmsnorm(d);
+    if (s != FQ_OK)
+        return s;
+    if (bytes)
+        *bytes = d->rows == 0 || d->cols == 0 ? 0 : rmsnorm_workspace(d->rows, d->cols);
+    return FQ_OK;
+}
+
+fq_status fq_rmsnorm_backward(const fq_rmsnorm_desc* d, const void* h, const float* rstd, const void* weight,
+                              const void* dy, const void* dres, void* dx, float* dweight, void* ws, size_t ws_bytes,
+                              hipStream_t st)
+{
+    const fq_status s = check_rmsnorm(d);
+    if (s != FQ_OK)
+        return s;
+    if (d->cols == 0 || (d->rows == 0 && (!dweight || d->accumulate)))
+        return FQ_OK;
+    if (d->rows > 0 && (!h || !rstd || !weight || !dy || !dx))
+        return FQ_E_INVALID;
+    if (!aligned(h, 16) || !aligned(rstd, 4) || !aligned(weight, 16) || !aligned(dy, 16) || !aligned(dres, 16) ||
+        !aligned(dx, 16) || !aligned(dweight, 16))
+        return FQ_E_ALIGN;
+    if (dweight && d->rows > 0) {
+        if (!ws || ws_bytes < rmsnorm_workspace(d->rows, d->cols))
+            return FQ_E_WORKSPACE;
+        if (!aligned(ws, 16))
+            return FQ_E_ALIGN;
+    }
+    NormBackArgs a;
+    a.rows = d->rows;
+    a.cols = d->cols;
+    a.h = h;
+    a.rstd = rstd;
+    a.w = weight;
+    a.dy = dy;
+    a.dres = dres;
+    a.dx = dx;
+    a.dw = dweight;
+    a.h_bf = d->h_dtype == FQ_IN_BF16;
+    a.w_bf = d->weight_dtype == FQ_IN_BF16;
+    a.dy_bf = d->y_dtype == FQ_IN_BF16;
+    a.acc = d->accumulate;
+    a.ws = (float*)ws;
+    return hip_status(launch_rmsnorm_backward(a, st));
+}
+
+// `wide`: columns of the result and its planes.
+static fq_status swiglu_args(const fq_swiglu_desc* d, const fq_desc* planes, const fq_quantized* out, int wide,
+                             SwigluArgs& a)
+{
+    if (!d || d->rows < 0 || d->cols < 0 || !in_dtype(d->x_dtype) || !in_dtype(d->y_dtype))
+        return FQ_E_INVALID;
+    if (d->cols % 8 || (d->cols > 0 && d->rows > kMaxElems / 2 / d->cols))
+        return FQ_E_SHAPE;
+    a.x_stride = d->x_stride;
+    fq_status s = check_stride(a.x_stride, 2 * d->cols, d->rows, d->x_dtype);
+    if (s != FQ_OK)
+        return s;
+    if (planes) {
+        if ((s = check_planes(planes, out, d->rows, wide * d->cols, a.kind)) != FQ_OK)
+            return s;
+        if (d->cols % planes->block_cols)
+            return FQ_E_SHAPE;
+        set_planes(a, planes, out);
+    }
+    a.rows = d->rows;
+    a.cols = d->cols;
+    a.x_bf = d->x_dtype == FQ_IN_BF16;
+    return FQ_OK;
+}
+
+fq_status fq_swiglu(const fq_swiglu_desc* d, const fq_desc* planes, const void* x, void* y, const fq_quantized* out,
+                    hipStream_t st)
+{
+    SwigluArgs a;
+    const fq_status s = swiglu_args(d, planes, out, 1, a);
+    if (s != FQ_OK)
+        return s;
+    if (d->rows == 0 || d->cols == 0)
+        return FQ_OK;
+    if (!planes && !y)
+        return FQ_E_INVALID;
+    if (!x)
+        return FQ_E_INVALID;
+    if (!aligned(x, 16) || !aligned(y, 16))
+        return FQ_E_ALIGN;
+    a.x = x;
+    a.y = y;
+    a.y_bf = d->y_dtype == FQ_IN_BF16;
+    return hip_status(launch_swiglu(a, st));
+}
+
+fq_status fq_swiglu_backward(const fq_swiglu_desc* d, const fq_desc* planes, const void* x, const void* dy, void* dx,
+                             const fq_quantized* out, hipStream_t st)
+{
+    SwigluArgs a;
+    const fq_status s = swiglu_args(d, planes, out, 2, a);
+    if (s != FQ_OK)
+        return s;
+    if (d->rows == 0 || d->cols == 0)
+        return FQ_OK;
+    if (!planes && !dx)
+        return FQ_E_INVALID;
+    if (!x || !dy)
+        return FQ_E_INVALID;
+    if (!aligned(x, 16) || !aligned(dy, 16) || !aligned(dx, 16))
+        return FQ_E_ALIGN;
+    a.x = x;
+    a.dy = dy;
+    a.y = dx;
+    a.dy_bf = d->y_dtype == FQ_IN_BF16;
+    a.y_bf = a.x_bf;
+    return hip_status(launch_swiglu(a, st));
 }
 
 }  // extern "C"

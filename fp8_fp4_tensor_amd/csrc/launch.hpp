@@ -204,6 +204,77 @@ struct GemmArgs {
 // Workspace bytes of a product of this shape (m, n, k, b1 and bf set).
 size_t gemm_workspace(const GemmArgs& g);
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream);
+// C = the sum of `splits` partial products in ws, [m, n] fp32 each (or C += ; zeros for none).
+hipError_t launch_gemm_join(const GemmArgs& g, int splits, hipStream_t stream);
+
+// The product of MX planes, C = A B^T (k_gemm_mx.hip).
+struct GemmMxArgs {
+    int64_t m = 0, n = 0, k = 0;     // m, n >= 1; k a multiple of 32
+    int fa = 0, fb = 0;              // element formats (0 E4M3, 1 E5M2, 2 E2M1)
+    const uint8_t* a = nullptr;      // [m, k] codes (two E2M1 a byte)
+    const uint8_t* sa = nullptr;     // [m, k/32] E8M0
+    const uint8_t* b = nullptr;      // [n, k]
+    const uint8_t* sb = nullptr;     // [n, k/32]
+    void* c = nullptr;               // [m, n] fp32, or bf16 if bf
+    int bf = 0, acc = 0;             // acc: C += (fp32 only)
+    uint8_t* ws = nullptr;
+};
+// Workspace bytes of a product of this shape (m, n, k, fa, fb and bf set).
+size_t gemm_mx_workspace(const GemmMxArgs& g);
+hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream);
+
+// The recipe of the planes that an operator quantizes its result to.
+enum PlaneKind : int { kMxE4M3 = 0, kMxE5M2, kMxE2M1, kBlockFp32, kBlockPow2, kNoPlanes };
+
+// Root-mean-square norm (k_norm.hip). Types are flags: 1 bf16, 0 fp32.
+struct NormArgs {
+    int64_t rows = 0, cols = 0, x_stride = 0;
+    const void* x = nullptr;         // [rows, cols], rows x_stride elements apart
+    const void* res = nullptr;       // [rows, cols] of h's type, or null
+    const void* w = nullptr;         // [cols]
+    void* h = nullptr;               // x + res, with res
+    float* rstd = nullptr;           // [rows], or null without qt
+    void* y = nullptr;               // [rows, cols], or null
+    bool x_bf = false, h_bf = false, w_bf = false, y_bf = false;
+    float eps = 0.0f;
+    int kind = 0;                    // PlaneKind of the planes
+    uint8_t* q = nullptr;            // rowwise codes and scales, or null
+    void* s = nullptr;
+    uint8_t* qt = nullptr;           // colwise
+    void* st = nullptr;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+struct NormBackArgs {
+    int64_t rows = 0, cols = 0;
+    const void* h = nullptr;         // [rows, cols]
+    const float* rstd = nullptr;
+    const void* w = nullptr;
+    const void* dy = nullptr;        // [rows, cols]
+    const void* dres = nullptr;      // [rows, cols] of h's type, or null
+    void* dx = nullptr;              // [rows, cols] of h's type
+    float* dw = nullptr;             // [cols], or null
+    bool h_bf = false, w_bf = false, dy_bf = false;
+    int acc = 0;                     // dw +=
+    float* ws = nullptr;             // rmsnorm_workspace() bytes, with dw
+};
+size_t rmsnorm_workspace(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_backward(const NormBackArgs& a, hipStream_t stream);
+
+// The gated activation, or its gradient if dy is given (k_swiglu.hip).
+struct SwigluArgs {
+    int64_t rows = 0, cols = 0, x_stride = 0;
+    const void* x = nullptr;         // [rows, 2 * cols], rows x_stride elements apart: gate, up
+    const void* dy = nullptr;        // [rows, cols]
+    void* y = nullptr;               // [rows, cols], with dy the gradient [rows, 2 * cols]; or null
+    bool x_bf = false, dy_bf = false, y_bf = false;
+    int kind = 0;                    // planes of y, as above
+    uint8_t* q = nullptr;
+    void* s = nullptr;
+    uint8_t* qt = nullptr;
+    void* st = nullptr;
+};
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t stream);
 
 // One 8-bit key/value cache and the sequences a call touches (k_kv.hip, k_attn.hip).
 struct KvArgs {

@@ -77,6 +77,22 @@ class FqAttentionDesc(ctypes.Structure):
                 ("softcap", ctypes.c_float), ("q_stride", ctypes.c_int64)]
 
 
+class FqGemmMxDesc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("a_format", ctypes.c_int32),
+                ("b_format", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class FqRmsnormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("h_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64)]
+
+
+class FqSwigluDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64)]
+
+
 class FqError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -103,6 +119,9 @@ def lib():
     cp = ctypes.POINTER(FqKvCache)
     bp = ctypes.POINTER(FqKvBatch)
     ap = ctypes.POINTER(FqAttentionDesc)
+    mp = ctypes.POINTER(FqGemmMxDesc)
+    np_ = ctypes.POINTER(FqRmsnormDesc)
+    sp = ctypes.POINTER(FqSwigluDesc)
     sig = {
         "fq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "fq_sizes": (ctypes.c_int, [dp, _SZ, _SZ, _SZ, _SZ, _SZ]),
@@ -119,6 +138,13 @@ def lib():
         "fq_kv_append": (ctypes.c_int, [cp, bp, ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
         "fq_attention_workspace": (ctypes.c_int, [cp, bp, ap, _SZ]),
         "fq_attention": (ctypes.c_int, [cp, bp, ap, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+        "fq_gemm_mx_workspace": (ctypes.c_int, [mp, _SZ]),
+        "fq_gemm_mx": (ctypes.c_int, [mp, pp, pp, _P, _P, ctypes.c_size_t, _P]),
+        "fq_rmsnorm": (ctypes.c_int, [np_, dp, _P, _P, _P, _P, _P, _P, qp, _P]),
+        "fq_rmsnorm_workspace": (ctypes.c_int, [np_, _SZ]),
+        "fq_rmsnorm_backward": (ctypes.c_int, [np_, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+        "fq_swiglu": (ctypes.c_int, [sp, dp, _P, _P, qp, _P]),
+        "fq_swiglu_backward": (ctypes.c_int, [sp, dp, _P, _P, _P, qp, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -545,3 +571,234 @@ def fq_attention(cache: KvCache, batch: KvBatch, d: FqAttentionDesc, q: torch.Te
     _check(lib().fq_attention(cache._ref, batch._ref, ctypes.byref(d), q.data_ptr(),
                               out.data_ptr(), None if lse is None else lse.data_ptr(),
                               None if ws is None else ws.data_ptr(), size, _stream(stream)), "fq_attention")
+
+
+# ---------------------------------------------------------------- a feed-forward block on microscaled data
+def _here(on: int, *tensors: Optional[torch.Tensor]):
+    """Tensors that are given are on GPU `on`, and that is the current one: a launch goes there."""
+    _one_gpu(on, *tensors)
+    if on != torch.cuda.current_device():
+        raise ValueError("the tensors of a call are on the current GPU")
+
+
+class MxPlane(_Handle):
+    """One MX copy as an operand: codes of `fmt` [rows, k] (or [rows, k / 2] packed) and E8M0 scales (kept alive here)."""
+
+    def __init__(self, data: torch.Tensor, scale: torch.Tensor, fmt: int):
+        if not (data.is_contiguous() and scale.is_contiguous()):
+            raise ValueError("planes are contiguous")
+        if fmt == FQ_E2M1:
+            if data.dtype != torch.uint8:
+                raise TypeError("packed codes are bytes")
+        else:
+            _codes_of(fmt, data)
+        if scale.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+            raise TypeError("MX scales are E8M0 bytes")
+        c = FqPlane(data.data_ptr(), scale.data_ptr())
+        self.__dict__.update(data=data, scale=scale, fmt=fmt, _sizes=(data.numel(), scale.numel()),
+                             _on=_common_gpu(data, scale), _c=c, _ref=ctypes.byref(c))
+
+    @classmethod
+    def rowwise(cls, q: Quantized, fmt: int) -> "MxPlane":
+        return cls(q.row_data, q.row_scale, fmt)
+
+    @classmethod
+    def colwise(cls, q: Quantized, fmt: int) -> "MxPlane":
+        return cls(q.col_data, q.col_scale, fmt)
+
+
+def gemm_mx_desc(m: int, n: int, k: int, a_format: int = FQ_E4M3, b_format: int = FQ_E4M3,
+                 out_dtype: int = FQ_IN_BF16, accumulate: bool = False) -> FqGemmMxDesc:
+    return FqGemmMxDesc(m, n, k, a_format, b_format, out_dtype, int(accumulate))
+
+
+def fq_gemm_mx_workspace(d: FqGemmMxDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().fq_gemm_mx_workspace(ctypes.byref(d), ctypes.byref(n)), "fq_gemm_mx_workspace")
+    return n.value
+
+
+def alloc_gemm_mx_workspace(d: FqGemmMxDesc, device="cuda") -> Optional[torch.Tensor]:
+    n = fq_gemm_mx_workspace(d)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def fq_gemm_mx(d: FqGemmMxDesc, a: MxPlane, b: MxPlane, out: torch.Tensor, ws: Optional[torch.Tensor] = None,
+               stream=None):
+    """out [m, n] = A B^T of two MX planes (out += with d.accumulate)."""
+    m, n, k = d.m, d.n, d.k
+    if a.fmt != d.a_format or b.fmt != d.b_format:
+        raise TypeError("planes are of the descriptor's formats")
+    if a._sizes != (m * k >> (a.fmt == FQ_E2M1), m * (k // 32)) or b._sizes != (n * k >> (b.fmt == FQ_E2M1), n * (k // 32)):
+        raise ValueError("a is [m, k] and b is [n, k], with a scale for each 32 of a row")
+    if out.numel() != m * n:
+        raise ValueError("out is [m, n]")
+    if in_dtype_of(out) != d.out_dtype or not out.is_contiguous():
+        raise TypeError("out is contiguous and of the descriptor's out_dtype")
+    size = _nbytes(ws)
+    _here(a._on if a._on == b._on else -1, out, ws)
+    _check(lib().fq_gemm_mx(ctypes.byref(d), a._ref, b._ref, out.data_ptr(), None if ws is None else ws.data_ptr(), size,
+                            _stream(stream)), "fq_gemm_mx")
+
+
+class Planes(_Handle):
+    """What an operator quantizes its result to: a descriptor and the buffers alloc_quantized gives for it."""
+
+    def __init__(self, d: FqDesc, out: Quantized):
+        z = fq_sizes(d)
+        sd = _scale_dtype(d)
+        given = []
+        for want, t, dtype in ((z.row_data, out.row_data, torch.uint8), (z.row_scale, out.row_scale, sd),
+                               (z.col_data, out.col_data, torch.uint8), (z.col_scale, out.col_scale, sd)):
+            if not want:
+                continue
+            if t is None or t.numel() * t.element_size() != want or not t.is_contiguous():
+                raise ValueError("the planes have the sizes that fq_sizes reports, and are contiguous")
+            if t.dtype != dtype:
+                raise TypeError("codes are bytes, scales bytes (MX) or float32")
+            given.append(t)
+        copy = FqDesc.from_buffer_copy(d)  # the caller's may change
+        q = FqQuantized(FqPlane(_ptr(out.row_data) if z.row_data else None, _ptr(out.row_scale) if z.row_scale else None),
+                        FqPlane(_ptr(out.col_data) if z.col_data else None, _ptr(out.col_scale) if z.col_scale else None),
+                        None, None)
+        self.__dict__.update(out=out, rows=d.rows, cols=d.cols, _keep=given, _on=_common_gpu(*given) if given else -1,
+                             _empty=not given, _d=copy, _q=q, _dref=ctypes.byref(copy), _qref=ctypes.byref(q))
+
+
+def _rows2(t: torch.Tensor, rows: int, cols: int, dtype: int, what: str):
+    if t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{what} is contiguous [{rows}, {cols}]")
+    if in_dtype_of(t) != dtype:
+        raise TypeError(f"{what} is of the descriptor's type")
+
+
+def _row_stride(t: torch.Tensor, rows: int, cols: int, dtype: int, what: str) -> int:
+    """The row stride of a [rows, cols] tensor whose rows are each contiguous, 0 if the tensor is."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} is [{rows}, {cols}]")
+    if in_dtype_of(t) != dtype:
+        raise TypeError(f"{what} is of the descriptor's type")
+    if t.is_contiguous():
+        return 0
+    step, one = t.stride()
+    if one != 1 or step < cols:
+        raise ValueError(f"{what}: rows are contiguous and do not overlap")
+    return step
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype: int, what: str):
+    if t is not None and (t.numel() != n or not t.is_contiguous() or in_dtype_of(t) != dtype):
+        raise TypeError(f"{what} is contiguous, of {n} values and of its type")
+
+
+def _target(planes: Optional[Planes], rows: int, cols: int, y: Optional[torch.Tensor], x: torch.Tensor) -> int:
+    """The GPU of the results (x's own where there is nothing to write)."""
+    if planes is None:
+        if y is None:
+            raise ValueError("nothing to write: neither planes nor a high-precision result")
+        return y.get_device()
+    if (planes.rows, planes.cols) != (rows, cols):
+        raise ValueError(f"planes are of [{rows}, {cols}]")
+    return x.get_device() if planes._empty else planes._on
+
+
+def rmsnorm_desc(rows: int, cols: int, x_dtype: int = FQ_IN_BF16, h_dtype: int = FQ_IN_BF16,
+                 weight_dtype: int = FQ_IN_F32, y_dtype: int = FQ_IN_BF16, eps: float = 1e-6,
+                 accumulate: bool = False) -> FqRmsnormDesc:
+    return FqRmsnormDesc(rows, cols, x_dtype, h_dtype, weight_dtype, y_dtype, int(accumulate), eps, 0)
+
+
+def fq_rmsnorm(d: FqRmsnormDesc, x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+               h: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               planes: Optional[Planes] = None, stream=None):
+    """h = x + residual, rstd = 1 / sqrt(mean h^2 + eps), y = h * rstd * weight, and planes of y. Without a residual
+    h is x. The row stride is x's own, whatever d.x_stride holds."""
+    rows, cols = d.rows, d.cols
+    on = _target(planes, rows, cols, y, x)
+    stride = _row_stride(x, rows, cols, d.x_dtype, "x")
+    if (residual is None) != (h is None):
+        raise ValueError("residual and h go together")
+    if residual is not None:
+        _rows2(residual, rows, cols, d.h_dtype, "residual")
+        _rows2(h, rows, cols, d.h_dtype, "h")
+    if y is not None:
+        _rows2(y, rows, cols, d.y_dtype, "y")
+    _vector(weight, cols, d.weight_dtype, "weight")
+    _vector(rstd, rows, FQ_IN_F32, "rstd")
+    _here(on, x, weight, residual, h, rstd, y)
+    if stride != d.x_stride:  # a descriptor of this call: the caller's may be in use elsewhere
+        d = FqRmsnormDesc.from_buffer_copy(d)
+        d.x_stride = stride
+    _check(lib().fq_rmsnorm(ctypes.byref(d), None if planes is None else planes._dref, x.data_ptr(),
+                            None if residual is None else residual.data_ptr(), weight.data_ptr(),
+                            None if h is None else h.data_ptr(), None if rstd is None else rstd.data_ptr(),
+                            None if y is None else y.data_ptr(), None if planes is None else planes._qref,
+                            _stream(stream)), "fq_rmsnorm")
+
+
+def fq_rmsnorm_workspace(d: FqRmsnormDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().fq_rmsnorm_workspace(ctypes.byref(d), ctypes.byref(n)), "fq_rmsnorm_workspace")
+    return n.value
+
+
+def alloc_rmsnorm_workspace(d: FqRmsnormDesc, device="cuda") -> Optional[torch.Tensor]:
+    n = fq_rmsnorm_workspace(d)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def fq_rmsnorm_backward(d: FqRmsnormDesc, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
+                        dx: torch.Tensor, dweight: Optional[torch.Tensor] = None, dres: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None):
+    """dx (of x and of the residual) and dweight (fp32, += with d.accumulate) from dy and, past the norm, dres."""
+    rows, cols = d.rows, d.cols
+    _rows2(h, rows, cols, d.h_dtype, "h")
+    _rows2(dy, rows, cols, d.y_dtype, "dy")
+    _rows2(dx, rows, cols, d.h_dtype, "dx")
+    if dres is not None:
+        _rows2(dres, rows, cols, d.h_dtype, "dres")
+    _vector(rstd, rows, FQ_IN_F32, "rstd")
+    _vector(weight, cols, d.weight_dtype, "weight")
+    _vector(dweight, cols, FQ_IN_F32, "dweight")
+    size = _nbytes(ws)
+    _here(h.get_device(), rstd, weight, dy, dx, dweight, dres, ws)
+    _check(lib().fq_rmsnorm_backward(ctypes.byref(d), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), dy.data_ptr(),
+                                     None if dres is None else dres.data_ptr(), dx.data_ptr(),
+                                     None if dweight is None else dweight.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), size, _stream(stream)), "fq_rmsnorm_backward")
+
+
+def swiglu_desc(rows: int, cols: int, x_dtype: int = FQ_IN_BF16, y_dtype: int = FQ_IN_BF16) -> FqSwigluDesc:
+    return FqSwigluDesc(rows, cols, x_dtype, y_dtype, 0)
+
+
+def _swiglu_x(d: FqSwigluDesc, x: torch.Tensor) -> FqSwigluDesc:
+    stride = _row_stride(x, d.rows, 2 * d.cols, d.x_dtype, "x")
+    return d if stride == d.x_stride else FqSwigluDesc(d.rows, d.cols, d.x_dtype, d.y_dtype, stride)
+
+
+def fq_swiglu(d: FqSwigluDesc, x: torch.Tensor, y: Optional[torch.Tensor] = None, planes: Optional[Planes] = None,
+              stream=None):
+    """y = silu(gate) * up of x = [gate | up], and planes of y. The row stride is x's own."""
+    on = _target(planes, d.rows, d.cols, y, x)
+    if y is not None:
+        _rows2(y, d.rows, d.cols, d.y_dtype, "y")
+    d = _swiglu_x(d, x)
+    _here(on, x, y)
+    _check(lib().fq_swiglu(ctypes.byref(d), None if planes is None else planes._dref, x.data_ptr(),
+                           None if y is None else y.data_ptr(), None if planes is None else planes._qref,
+                           _stream(stream)), "fq_swiglu")
+
+
+def fq_swiglu_backward(d: FqSwigluDesc, x: torch.Tensor, dy: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                       planes: Optional[Planes] = None, stream=None):
+    """dx = [dgate | dup] from x = [gate | up] and dy, and planes of it. The row stride is x's own."""
+    on = _target(planes, d.rows, 2 * d.cols, dx, x)
+    _rows2(dy, d.rows, d.cols, d.y_dtype, "dy")
+    if dx is not None:
+        _rows2(dx, d.rows, 2 * d.cols, d.x_dtype, "dx")
+    d = _swiglu_x(d, x)
+    _here(on, x, dy, dx)
+    _check(lib().fq_swiglu_backward(ctypes.byref(d), None if planes is None else planes._dref, x.data_ptr(),
+                                    dy.data_ptr(), None if dx is None else dx.data_ptr(),
+                                    None if planes is None else planes._qref, _stream(stream)), "fq_swiglu_backward")

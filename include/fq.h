@@ -574,6 +574,139 @@ fq_status fq_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, const
                        const void *q, void *out, float *lse, void *workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A feed-forward block on microscaled data
+ * ---------------------------------------------------------------------------
+ *
+ * The matrix product of two MX planes,
+ *
+ *   C[i,j] = sum_b 2^(ea[i,b]-127) * 2^(eb[j,b]-127) * sum_{t<32} A[i, 32b+t] * B[j, 32b+t]
+ *
+ * A: [m, k] codes of a_format, B: [n, k] codes of b_format, each FQ_E4M3,
+ * FQ_E5M2 or FQ_E2M1 (packed two per byte), with E8M0 codes [m, k/32] and
+ * [n, k/32]: planes as FQ_MX writes them. With rowwise and colwise planes of
+ * the activations X, the weights W and the gradients dY of Y = X W^T,
+ *   forward  Y  [T,O]   a = X's rowwise plane,  b = W's rowwise plane
+ *   dgrad    dX [T,I]   a = dY's rowwise plane, b = W's colwise plane
+ *   wgrad    dW [O,I]   a = dY's colwise plane, b = X's colwise plane
+ * The result is rounded once to out_dtype from fp32 sums. With 8-bit elements
+ * on both sides and bf16 outputs the matrix instruction keeps each product to
+ * about 2^-12 of the largest of its 128 (1.5e-5 of the result in the mean
+ * square, against the output's rounding of 2^-9). fp32 outputs have products and sums in fp32
+ * throughout; there a value below 2^-126 in magnitude may count as zero.
+ *   accumulate   1: C += the product (FQ_IN_F32 only), 0: C = the product.
+ *   k % 32 == 0; m*k, n*k and m*n at most 2^36, k at most 2^22.
+ * k = 0 gives zeros (or leaves C with accumulate); m = 0 or n = 0 does nothing.
+ * Codes must be finite and scale codes below 255. The result does not depend
+ * on the run: no atomics, sums in a fixed order.
+ */
+typedef struct {
+    int64_t m, n, k;
+    int32_t a_format; /* fq_format of A's codes */
+    int32_t b_format;
+    int32_t out_dtype; /* fq_in_dtype of C */
+    int32_t accumulate;
+} fq_gemm_mx_desc;
+
+/* Device scratch bytes of fq_gemm_mx for this desc (0 for many shapes). */
+fq_status fq_gemm_mx_workspace(const fq_gemm_mx_desc *desc, size_t *workspace);
+
+/* C = A B^T as above; out is [m, n], row-major, 16-byte aligned. A NULL
+ * workspace is accepted where fq_gemm_mx_workspace reports 0. */
+fq_status fq_gemm_mx(const fq_gemm_mx_desc *desc, const fq_plane *a, const fq_plane *b, void *out, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual, rounded to h_dtype (without a residual h is x)
+ *   r = 1 / sqrt(mean_j h[j]^2 + eps)
+ *   y[j] = fp32(fp32(h[j] * r) * weight[j])
+ * and quantized planes of the fp32 y: the bytes that fq_quantize with the
+ * descriptor `planes` gives for that y.
+ *   rows, cols    cols % 8 == 0, cols <= 32768, rows*cols <= 2^36
+ *   x_dtype       fq_in_dtype of x
+ *   h_dtype       of residual and h; in the backward call of h, dres and dx
+ *   weight_dtype  of weight
+ *   y_dtype       of y (rounded to nearest even); in the backward call of dy
+ *   accumulate    backward only: 1: dweight += its value, 0: dweight =
+ *   eps           finite and positive
+ *   x_stride      elements between rows of x, 0: cols. A multiple of 8 (bf16) or 4.
+ * x     [rows, cols]; residual and h [rows, cols] contiguous, both or neither;
+ * h may be residual (or x, if contiguous and of one type): each element is read
+ * before it is written.
+ * rstd  [rows] fp32: r. Needed with colwise planes, otherwise may be NULL.
+ * y     [rows, cols] or NULL.
+ * planes, out   what to quantize to, or NULL for neither: recipe FQ_MX (any
+ * format), or FQ_BLOCK_FP32 with 1x128 tiles (either scale mode); rounding
+ * to nearest even, no transform; rows and cols those of the norm; rowwise, colwise or
+ * both. in_dtype, seed, offset and rht_signs are not read.
+ * At least one of y and the planes is asked for. The sum of a row's squares
+ * must be finite in fp32.
+ */
+typedef struct {
+    int64_t rows, cols;
+    int32_t x_dtype;
+    int32_t h_dtype;
+    int32_t weight_dtype;
+    int32_t y_dtype;
+    int32_t accumulate;
+    float eps;
+    int64_t x_stride;
+} fq_rmsnorm_desc;
+
+fq_status fq_rmsnorm(const fq_rmsnorm_desc *desc, const fq_desc *planes, const void *x, const void *residual,
+                     const void *weight, void *h, float *rstd, void *y, const fq_quantized *out, hipStream_t stream);
+
+/* Device scratch bytes of fq_rmsnorm_backward for this desc. */
+fq_status fq_rmsnorm_workspace(const fq_rmsnorm_desc *desc, size_t *workspace);
+
+/*
+ * The norm's gradients. With z = h * rstd and g = dy * weight,
+ *   dx[j]      = rstd * (g[j] - z[j] * mean_j(g z)) + dres[j]
+ *   dweight[j] = sum over rows of dy[j] * z[j]     (fp32; += with accumulate)
+ * h (x if the forward call had no residual), dres, dx: [rows, cols] of
+ * h_dtype, contiguous; dres is the gradient that reaches h past the norm, or
+ * NULL for none; dx is the gradient of x and of the residual alike, and may be
+ * dres or h or, of one type, dy. rstd: [rows] from the forward call. dy: [rows, cols] of y_dtype.
+ * dweight: [cols] fp32, 16-byte aligned, or NULL (then the workspace may be
+ * NULL too). x_dtype, x_stride and eps are not used. Sums are in a fixed
+ * order that depends on rows and cols alone.
+ */
+fq_status fq_rmsnorm_backward(const fq_rmsnorm_desc *desc, const void *h, const float *rstd, const void *weight,
+                              const void *dy, const void *dres, void *dx, float *dweight, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gated activation y = silu(gate) * up, silu(g) = g / (1 + exp(-g)), in
+ * fp32, and quantized planes of the fp32 y.
+ *   x         [rows, 2 * cols] of x_dtype, rows x_stride elements apart (0:
+ *             2 * cols): a row's gate, then its up
+ *   y         [rows, cols] of y_dtype, or NULL
+ *   planes, out   as for fq_rmsnorm, of [rows, cols]
+ *   cols % 8 == 0, 2*rows*cols <= 2^36; x_stride a multiple of 8 (bf16) or 4.
+ */
+typedef struct {
+    int64_t rows, cols;
+    int32_t x_dtype;
+    int32_t y_dtype; /* of y; in the backward call of dy */
+    int64_t x_stride;
+} fq_swiglu_desc;
+
+fq_status fq_swiglu(const fq_swiglu_desc *desc, const fq_desc *planes, const void *x, void *y, const fq_quantized *out,
+                    hipStream_t stream);
+
+/*
+ * Its gradient. With s = 1 / (1 + exp(-gate)),
+ *   dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s
+ *   dy    [rows, cols] of y_dtype
+ *   dx    [rows, 2 * cols] of x_dtype, contiguous: dgate, then dup; or NULL
+ *   planes, out   of the fp32 dx, [rows, 2 * cols] (planes->cols = 2 * cols,
+ *                 cols a multiple of the block)
+ */
+fq_status fq_swiglu_backward(const fq_swiglu_desc *desc, const fq_desc *planes, const void *x, const void *dy, void *dx,
+                             const fq_quantized *out, hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char *fq_status_str(fq_status status);
 
