@@ -28,7 +28,8 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=
          "-Wall", "-Wno-unused-function", "-I", INCLUDE, "-I", CSRC]
 
 SOURCES = ["api.cpp", "k_tensor.hip", "k_block.hip", "k_mx.hip", "k_mxfp4.hip", "k_nvfp4.hip", "k_dequant.hip", "k_requant.hip",
-           "k_sr8.hip", "k_gemm.hip", "k_gemm_mx.hip", "k_norm.hip", "k_swiglu.hip", "k_kv.hip", "k_attn.hip", "noalloc.hip"]
+           "k_sr8.hip", "k_gemm.hip", "k_gemm_mx.hip", "k_gemm_mx_e4m3.hip",
+           "k_gemm_mx_e5m2.hip", "k_gemm_mx_e2m1.hip", "k_norm.hip", "k_swiglu.hip", "k_kv.hip", "k_attn.hip", "noalloc.hip"]
 
 
 def _compile(src: str, verbose: bool) -> str:

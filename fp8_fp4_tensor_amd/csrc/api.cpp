@@ -924,7 +924,7 @@ static fq_status check_gemm_mx(const fq_gemm_mx_desc* d)
         return FQ_E_INVALID;
     if (d->accumulate && d->out_dtype != FQ_IN_F32)
         return FQ_E_UNSUPPORTED;
-    if (d->k % 32 || d->k > (int64_t(1) << 22))
+    if (d->k % 32 || d->k > (int64_t(1) << 22) || d->m > (int64_t(1) << 28) || d->n > (int64_t(1) << 28))
         return FQ_E_SHAPE;
     auto over = [](int64_t x, int64_t y) { return y > 0 && x > kMaxElems / y; };
     if (over(d->m, d->k) || over(d->n, d->k) || over(d->m, d->n))

@@ -9,8 +9,9 @@
 //
 // Operand order: B's rows are the instruction's rows and A's rows its columns,
 // so a lane holds one row i of C and four consecutive columns j.
-#include "launch.hpp"
+#include "gemm_mx.hpp"
 #include "mx_operand.hpp"
+#include "plan.hpp"
 
 namespace fq {
 namespace {
@@ -35,10 +36,9 @@ __device__ __forceinline__ i32x8 load128(const uint8_t* p, int64_t k0, int64_t k
     }
 }
 
-template <int FA, int FB, bool F32>
+template <int FA, int FB, bool WIDE>
 __global__ __launch_bounds__(kFewWaves * 64) void k_gemm_mx_few(GemmMxArgs a)
 {
-    constexpr bool WIDE = kWidened<FA, FB, F32>;
     __shared__ f32x4 part[kFewWaves][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int row = lane & 15, g = lane >> 4;
@@ -81,7 +81,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_gemm_mx_few(GemmMxArgs a)
 #pragma unroll
     for (int x = 1; x < kFewWaves; ++x)
         acc += part[x][lane];
-    store4<!F32>(a.c, m0 + row, n0 + g * 4, a.n, acc, a.acc);
+    if (a.bf)
+        store4<true>(a.c, m0 + row, n0 + g * 4, a.n, acc, false);
+    else
+        store4<false>(a.c, m0 + row, n0 + g * 4, a.n, acc, a.acc);
 }
 
 template <int FA, int FB>
@@ -89,32 +92,153 @@ hipError_t few(const GemmMxArgs& a, hipStream_t st)
 {
     const dim3 grid((unsigned)cdiv(a.n, 16), (unsigned)cdiv(a.m, 16));
     constexpr int th = kFewWaves * 64;
-    a.bf ? k_gemm_mx_few<FA, FB, false><<<grid, th, 0, st>>>(a) : k_gemm_mx_few<FA, FB, true><<<grid, th, 0, st>>>(a);
+    if (kWidened<FA, FB, true> && !a.bf)
+        k_gemm_mx_few<FA, FB, kWidened<FA, FB, true>><<<grid, th, 0, st>>>(a);
+    else
+        k_gemm_mx_few<FA, FB, false><<<grid, th, 0, st>>>(a);
     return hipGetLastError();
 }
 
+// Scales [rows, nb] of both operands -> words as MxTileArgs has them, zeros past
+// nb and past the last row of a group of 64: a wave takes 64 words of a group.
+struct ScalesArgs {
+    const uint8_t* from[2];
+    uint32_t* to[2];
+    int64_t rows[2], groups_a;
+    int nb, words;
+};
+
+__global__ __launch_bounds__(kWG) void k_gemm_mx_scales(ScalesArgs a)
+{
+    __shared__ uint32_t tile[64][65];
+    const int64_t group = blockIdx.x;
+    const int which = group < a.groups_a ? 0 : 1;
+    const int64_t g = which ? group - a.groups_a : group;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int first = blockIdx.y * 64, word = first + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t row = g * 64 + w * 16 + i;
+        uint32_t v = 0;
+        if (row < a.rows[which] && word < a.words) {
+            const uint8_t* p = a.from[which] + row * a.nb + 4 * word;
+            if ((a.nb & 3) == 0)
+                v = *(const uint32_t*)p;
+            else
+                for (int e = 0; e < 4; ++e)
+                    v |= 4 * word + e < a.nb ? (uint32_t)p[e] << 8 * e : 0u;
+        }
+        tile[w * 16 + i][lane] = v;
+    }
+    __syncthreads();
+    for (int i = 0; i < 16; ++i) {
+        const int at = first + w * 16 + i;
+        if (at < a.words)
+            a.to[which][(g * a.words + at) * 64 + lane] = tile[lane][w * 16 + i];
+    }
+}
+
 template <int FA>
-hipError_t with_b(const GemmMxArgs& a, hipStream_t st)
+hipError_t few_by_b(const GemmMxArgs& a, hipStream_t st)
 {
     return a.fb == kE4M3 ? few<FA, kE4M3>(a, st) : a.fb == kE5M2 ? few<FA, kE5M2>(a, st) : few<FA, kE2M1>(a, st);
 }
 
+hipError_t tiles(const MxTileArgs& x, int kind, int splits, hipStream_t st)
+{
+    return x.g.fa == kE4M3   ? launch_mx_tiles_e4m3(x, kind, splits, st)
+           : x.g.fa == kE5M2 ? launch_mx_tiles_e5m2(x, kind, splits, st)
+                             : launch_mx_tiles_e2m1(x, kind, splits, st);
+}
+
+MxPlan plan_of(const GemmMxArgs& g)
+{
+    return plan_gemm_mx(g.m, g.n, g.k, g.fa == kE2M1, g.fb == kE2M1, g.bf);
+}
+
+// Workspace: arranged scales of A, of B, then partial sums.
+size_t arranged_bytes(int64_t rows, int64_t words) { return (size_t)(cdiv(rows, 64) * words) * 256; }
+
+// The rows that x.g names, by one kind of tile.
+hipError_t part(MxTileArgs x, int kind, int splits, hipStream_t st)
+{
+    x.out = splits > 1 ? kOutPart : x.g.bf ? kOutBf16 : kOutF32;
+    const hipError_t e = tiles(x, kind, splits, st);
+    if (e != hipSuccess || splits == 1)
+        return e;
+    GemmArgs j;
+    j.m = x.g.m;
+    j.n = x.g.n;
+    j.c = x.g.c;
+    j.bf = x.g.bf;
+    j.acc = x.g.acc;
+    j.ws = x.part;
+    return launch_gemm_join(j, splits, st);
+}
+
 }  // namespace
 
-size_t gemm_mx_workspace(const GemmMxArgs&) { return 0; }
-
-hipError_t launch_gemm_mx(const GemmMxArgs& a, hipStream_t st)
+size_t gemm_mx_workspace(const GemmMxArgs& g)
 {
-    if (a.k == 0) {
-        GemmArgs g;
-        g.m = a.m;
-        g.n = a.n;
-        g.c = a.c;
-        g.bf = a.bf;
-        g.acc = a.acc;
-        return launch_gemm_join(g, 0, st);
+    if (g.k == 0)
+        return 0;
+    const MxPlan p = plan_of(g);
+    const int64_t words = cdiv(g.k, 128);
+    return (p.arranged ? arranged_bytes(g.m, words) + arranged_bytes(g.n, words) : 0) +
+           (p.splits > 1 ? (size_t)p.splits * (g.m - p.main) * g.n * sizeof(float) : 0);
+}
+
+hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t st)
+{
+    if (g.k == 0) {
+        GemmArgs j;
+        j.m = g.m;
+        j.n = g.n;
+        j.c = g.c;
+        j.bf = g.bf;
+        j.acc = g.acc;
+        return launch_gemm_join(j, 0, st);
     }
-    return a.fa == kE4M3 ? with_b<kE4M3>(a, st) : a.fa == kE5M2 ? with_b<kE5M2>(a, st) : with_b<kE2M1>(a, st);
+    const MxPlan p = plan_of(g);
+    if (p.kind < 0)
+        return g.fa == kE4M3 ? few_by_b<kE4M3>(g, st) : g.fa == kE5M2 ? few_by_b<kE5M2>(g, st) : few_by_b<kE2M1>(g, st);
+    MxTileArgs x;
+    x.g = g;
+    x.words = (int)cdiv(g.k, 128);
+    x.sa = (const uint32_t*)g.sa;
+    x.sb = (const uint32_t*)g.sb;
+    x.arranged = p.arranged;
+    uint8_t* ws = g.ws;
+    if (p.arranged) {
+        ScalesArgs s;
+        s.from[0] = g.sa;
+        s.from[1] = g.sb;
+        s.to[0] = (uint32_t*)ws;
+        s.to[1] = (uint32_t*)(ws + arranged_bytes(g.m, x.words));
+        s.rows[0] = g.m;
+        s.rows[1] = g.n;
+        s.groups_a = cdiv(g.m, 64);
+        s.nb = (int)(g.k / 32);
+        s.words = x.words;
+        k_gemm_mx_scales<<<dim3((unsigned)(s.groups_a + cdiv(g.n, 64)), (unsigned)cdiv(x.words, 64)), kWG, 0, st>>>(s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        x.sa = s.to[0];
+        x.sb = s.to[1];
+        ws += arranged_bytes(g.m, x.words) + arranged_bytes(g.n, x.words);
+    }
+    x.part = (float*)ws;
+    if (p.main == 0)
+        return part(x, p.kind, p.splits, st);
+    MxTileArgs rest = x;
+    x.g.m = p.main;
+    rest.g.m = g.m - p.main;
+    rest.g.a += (g.fa == kE2M1 ? p.main * g.k / 2 : p.main * g.k);
+    rest.sa += p.main * x.words;
+    rest.g.c = (char*)g.c + p.main * g.n * (g.bf ? 2 : 4);
+    const hipError_t e = part(x, 0, 1, st);
+    return e == hipSuccess ? part(rest, p.kind, p.splits, st) : e;
 }
 
 }  // namespace fq

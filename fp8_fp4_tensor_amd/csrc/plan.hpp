@@ -108,6 +108,95 @@ inline GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool bf)
     return rest;
 }
 
+// ---------------------------------------------------------------- products of MX planes
+constexpr int kChipCus = 256;
+
+// Tiles, and the time of one step (128 bytes of a row; 128 elements with one
+// 4-bit side) in us, alone on a CU and with as many as fit: both sides 8-bit,
+// both 4-bit, one of each, and widened (fp32 results with an 8-bit side).
+// From outputs of one round of the chip and depths of 2048 and 6144.
+struct MxTileCost {
+    int tm, tn, per_cu;
+    double alone[4], full[4];
+};
+constexpr MxTileCost kMxTiles[] = {
+    {256, 256, 1, {1.50, 1.75, 1.50, 2.75}, {1.50, 1.75, 1.50, 2.75}},
+    {128, 256, 1, {1.15, 1.41, 1.03, 1.60}, {1.15, 1.41, 1.03, 1.60}},
+    {64, 128, 2, {0.50, 0.63, 0.47, 0.73}, {1.03, 1.18, 0.97, 1.22}},
+    {64, 64, 3, {0.36, 0.43, 0.34, 0.56}, {0.98, 1.08, 0.90, 1.16}},
+};
+constexpr int kMxTileKinds = 4;
+
+struct MxPlan {
+    int kind = -1;     // index of kMxTiles, -1: k_gemm_mx_few
+    int splits = 1;
+    double us = 0.0;   // by the ranking
+    int64_t main = 0;  // leading rows that go to 256x256 tiles first, a multiple of 256
+    bool arranged = false;  // scales are laid out for the tiles first
+};
+
+inline MxPlan plan_gemm_mx_part(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bool bf)
+{
+    MxPlan best;
+    const int cost = a4 && b4 ? 1 : !bf ? 3 : a4 || b4 ? 2 : 0;
+    const int64_t steps = ceil_div(k, a4 && b4 ? 256 : 128);
+    if (m <= 16 && n <= 8192)
+        return best;
+    constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const double bytes = (double)m * (a4 ? k / 2 : k) + (double)n * (b4 ? k / 2 : k) + (double)(m + n) * k / 32 +
+                         (double)m * n * (bf ? 2 : 4);
+    for (int t = 0; t < kMxTileKinds; ++t) {
+        const MxTileCost& c = kMxTiles[t];
+        const int64_t tiles = ceil_div(m, c.tm) * ceil_div(n, c.tn);
+        for (int s : kSplits) {
+            if (s > 1 && (steps / s < 2 || tiles >= 1024 || (double)s * m * n * 4 > 128e6))
+                break;
+            const int64_t per_cu = ceil_div(tiles * s, kChipCus);  // workgroups of the busiest CU
+            const int64_t rounds = per_cu / c.per_cu, left = per_cu % c.per_cu;
+            const double one = c.alone[cost], all = c.full[cost];
+            double step = rounds * all;
+            if (left)
+                step += c.per_cu == 1 ? one : one + (all - one) * (left - 1) / (c.per_cu - 1);
+            const double work = ceil_div(steps, s) * step, read = bytes / 5e6;
+            double us = work > read ? work + read / 4 : read + work / 4;  // overlapped, but not wholly
+            if (s > 1)
+                us += 3.0 + (double)s * m * n * 8 / 6e6;
+            if (best.kind < 0 || us < best.us) {
+                best.kind = t;
+                best.splits = s;
+                best.us = us;
+            }
+        }
+    }
+    return best;
+}
+
+inline MxPlan plan_gemm_mx(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bool bf)
+{
+    MxPlan best = plan_gemm_mx_part(m, n, k, a4, b4, bf);
+    // rows beyond whole rounds of 256x256 tiles, as in plan_gemm
+    const int64_t across = ceil_div(n, 256), whole = ceil_div(m, 256) * across / kChipCus;
+    if (best.kind == 0 && best.splits == 1 && whole >= 1) {
+        const int64_t main = whole * kChipCus / across * 256;
+        if (main > 0 && main < m) {
+            MxPlan rest = plan_gemm_mx_part(m - main, n, k, a4, b4, bf);
+            rest.us += plan_gemm_mx_part(main, n, k, a4, b4, bf).us + 2.0;
+            if (rest.kind >= 0 && rest.us < best.us) {
+                best = rest;
+                best.main = main;
+            }
+        }
+    }
+    // A row's scales as the plane has them are four (or eight) bytes a step, a
+    // line of memory each: half (for 4-bit sides all) as many lines again as the
+    // operands. Words laid out by rows first cost a launch.
+    const int64_t steps = ceil_div(k, a4 && b4 ? 256 : 128);
+    const int64_t rounds = ceil_div(ceil_div(best.main ? best.main : m, 256) * across, kChipCus);
+    const bool wide = !bf && !(a4 && b4);
+    best.arranged = best.kind >= 0 && (k % 128 != 0 || (!wide && (best.kind == 0 || best.main) && rounds * steps >= 48));
+    return best;
+}
+
 // ---------------------------------------------------------------- attention
 constexpr int kAttnStep = 64;     // keys a step of a wave takes
 constexpr int kAttnRows = 16;     // query rows of a workgroup of the kernel for few rows
