@@ -122,36 +122,60 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a)
 }
 
 // The colwise plane, a tile of 128 x 128 a workgroup.
-template <int P>
-__global__ __launch_bounds__(kWG) void k_rmsnorm_cols(NormArgs a)
+template <int P, bool BF>
+__global__ __launch_bounds__(kTileThreads) void k_rmsnorm_cols(NormArgs a)
 {
     __shared__ __align__(16) TileLds lds;
-    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t across = cdiv(a.cols, kTileSide), tiles = across * cdiv(a.rows, kTileSide);
     const void* h = a.res ? a.h : a.x;
-    const bool bf = a.res ? a.h_bf : a.x_bf;
     const int64_t pitch = a.res ? a.cols : a.x_stride;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int64_t tr, tc;
         tile_coords(t, across, tr, tc);
         const TileSpan span = tile_span(tr, tc, a.rows, a.cols);
-        const int64_t r = span.r0 + rg * 8, c = span.c0 + cg * 8;
-        float v[8][8], w[8];
-        const bool in = cg * 8 < span.cols;
-        if (in)
-            load8(a.w, a.w_bf, c, w);
+        const int64_t c = span.c0 + min(tile_col(), span.cols - 4);
+        Four<BF> raw[8];
+        float r[8], w[4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool ok = in && rg * 8 + i < span.rows;
-            if (ok)
-                load8(h, bf, (r + i) * pitch + c, v[i]);
-            const float s = ok ? a.rstd[r + i] : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[i][e] = ok ? (v[i][e] * s) * w[e] : 0.0f;
+            const int64_t row = span.r0 + min(tile_row() + i, span.rows - 1);
+            raw[i].load(h, row * pitch + c);
+            r[i] = a.rstd[row];
         }
-        tile_cols<P>(v, lds, span, a.rows, a.qt, a.st);
+        if (a.w_bf) {
+            Four<true> b;
+            b.load(a.w, c);
+            b.widen(w);
+        } else {
+            Four<false> b;
+            b.load(a.w, c);
+            b.widen(w);
+        }
+        float v[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            raw[i].widen(v[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[i][e] = (v[i][e] * r[i]) * w[e];
+        }
+        tile_planes<P>(v, lds, span, a.rows, a.cols, nullptr, nullptr, a.qt, a.st);
     }
+}
+
+template <bool BF>
+hipError_t cols(const NormArgs& a, hipStream_t st)
+{
+    const int64_t tiles = cdiv(a.rows, kTileSide) * cdiv(a.cols, kTileSide);
+    const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
+    switch (a.kind) {
+    case kMxE4M3: k_rmsnorm_cols<kMxE4M3, BF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kMxE5M2: k_rmsnorm_cols<kMxE5M2, BF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kMxE2M1: k_rmsnorm_cols<kMxE2M1, BF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kBlockFp32: k_rmsnorm_cols<kBlockFp32, BF><<<grid, kTileThreads, 0, st>>>(a); break;
+    default: k_rmsnorm_cols<kBlockPow2, BF><<<grid, kTileThreads, 0, st>>>(a); break;
+    }
+    return hipGetLastError();
 }
 
 template <int TPR, int NV>
@@ -299,16 +323,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st)
                                      : rows<1024, 4>(a, st);
     if (e != hipSuccess || !a.qt)
         return e;
-    const int64_t tiles = cdiv(a.rows, kTileSide) * cdiv(a.cols, kTileSide);
-    const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
-    switch (a.kind) {
-    case kMxE4M3: k_rmsnorm_cols<kMxE4M3><<<grid, kWG, 0, st>>>(a); break;
-    case kMxE5M2: k_rmsnorm_cols<kMxE5M2><<<grid, kWG, 0, st>>>(a); break;
-    case kMxE2M1: k_rmsnorm_cols<kMxE2M1><<<grid, kWG, 0, st>>>(a); break;
-    case kBlockFp32: k_rmsnorm_cols<kBlockFp32><<<grid, kWG, 0, st>>>(a); break;
-    default: k_rmsnorm_cols<kBlockPow2><<<grid, kWG, 0, st>>>(a); break;
-    }
-    return hipGetLastError();
+    return (a.res ? a.h_bf : a.x_bf) ? cols<true>(a, st) : cols<false>(a, st);
 }
 
 size_t rmsnorm_workspace(int64_t rows, int64_t cols) { return (size_t)(partial_rows(rows, cols) * cols) * sizeof(float); }

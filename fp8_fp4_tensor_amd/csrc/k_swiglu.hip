@@ -28,91 +28,104 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& rest)
     rest = g < 0.0f ? q : u;
 }
 
-// Planes and high-precision copy of a thread's 8x8 results, a tile of [R, C].
+// High-precision copy and planes of a tile of [R, C].
 template <int P>
-__device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][8], TileLds& lds, const TileSpan& t,
+__device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][4], TileLds& lds, const TileSpan& t,
                                      int64_t R, int64_t C)
 {
     if (a.y) {
-        const int c = (threadIdx.x & 15) * 8, r = (threadIdx.x >> 4) * 8;
+        const int c = tile_col(), r = tile_row();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c < t.cols && r + i < t.rows)
-                store8(a.y, a.y_bf, (t.r0 + r + i) * C + t.c0 + c, v[i]);
+                store4v(a.y, a.y_bf, (t.r0 + r + i) * C + t.c0 + c, v[i]);
     }
-    if constexpr (P != kNoPlanes) {
-        if (a.q)
-            tile_rows<P>(v, t, C, a.q, a.s);
-        if (a.qt)
-            tile_cols<P>(v, lds, t, R, a.qt, a.st);
-    }
+    if constexpr (P != kNoPlanes)
+        tile_planes<P>(v, lds, t, R, C, a.q, a.s, a.qt, a.st);
 }
 
-template <int P, bool BACK>
-__global__ __launch_bounds__(kWG) void k_swiglu(SwigluArgs a)
+// A 128x128 tile of gate, of up and with BACK of dy a workgroup.
+template <int P, bool BACK, bool XBF, bool DBF>
+__global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
 {
     __shared__ __align__(16) TileLds lds;
-    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t across = cdiv(a.cols, kTileSide), tiles = across * cdiv(a.rows, kTileSide);
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int64_t tr, tc;
         tile_coords(t, across, tr, tc);
         TileSpan span = tile_span(tr, tc, a.rows, a.cols);
-        const int64_t r = span.r0 + rg * 8, c = span.c0 + cg * 8;
-        float v[8][8], u[8][8];
+        const int64_t c = span.c0 + min(tile_col(), span.cols - 4);
+        Four<XBF> gate[8], up[8];
+        Four<DBF> dy[BACK ? 8 : 1];
+        TileRows<XBF> gates(a.x, span, a.x_stride, c), ups(a.x, span, a.x_stride, a.cols + c);
+        TileRows<DBF> dys(BACK ? a.dy : a.x, span, a.cols, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool ok = cg * 8 < span.cols && rg * 8 + i < span.rows;
-            if (ok) {
-                load8(a.x, a.x_bf, (r + i) * a.x_stride + c, v[i]);
-                load8(a.x, a.x_bf, (r + i) * a.x_stride + a.cols + c, u[i]);
-            }
-            float d[8];
+            gate[i] = gates.next();
+            up[i] = ups.next();
             if constexpr (BACK)
-                if (ok)
-                    load8(a.dy, a.dy_bf, (r + i) * a.cols + c, d);
+                dy[i] = dys.next();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float v[8][4], w[BACK ? 8 : 1][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gate = ok ? v[i][e] : 0.0f, up = ok ? u[i][e] : 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            float g[4], u[4], d[4];
+            gate[i].widen(g);
+            up[i].widen(u);
+            if constexpr (BACK)
+                dy[i].widen(d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
                 float s, rest;
-                sigmoid(gate, s, rest);
+                sigmoid(g[e], s, rest);
                 if constexpr (BACK) {
-                    const float dy = ok ? d[e] : 0.0f, ds = dy * s;
-                    v[i][e] = ds * up * __builtin_fmaf(gate, rest, 1.0f);
-                    u[i][e] = ds * gate;
+                    const float ds = d[e] * s;
+                    v[i][e] = ds * u[e] * __builtin_fmaf(g[e], rest, 1.0f);
+                    w[i][e] = ds * g[e];
+                    asm volatile("" : "+v"(w[i][e]));  // here: the compiler would keep both factors until its use
                 } else {
-                    v[i][e] = gate * s * up;
+                    v[i][e] = g[e] * s * u[e];
                 }
             }
+            // rows one after the other: all at once would hold their intermediate values too
+            __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (BACK) {
             emit<P>(a, v, lds, span, a.rows, 2 * a.cols);
             span.c0 += a.cols;
-            emit<P>(a, u, lds, span, a.rows, 2 * a.cols);
+            emit<P>(a, w, lds, span, a.rows, 2 * a.cols);
         } else {
             emit<P>(a, v, lds, span, a.rows, a.cols);
         }
     }
 }
 
-template <bool BACK>
+template <bool BACK, bool XBF, bool DBF>
 hipError_t run(const SwigluArgs& a, hipStream_t st)
 {
     const int64_t tiles = cdiv(a.rows, kTileSide) * cdiv(a.cols, kTileSide);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
     switch (a.q || a.qt ? a.kind : (int)kNoPlanes) {
-    case kMxE4M3: k_swiglu<kMxE4M3, BACK><<<grid, kWG, 0, st>>>(a); break;
-    case kMxE5M2: k_swiglu<kMxE5M2, BACK><<<grid, kWG, 0, st>>>(a); break;
-    case kMxE2M1: k_swiglu<kMxE2M1, BACK><<<grid, kWG, 0, st>>>(a); break;
-    case kBlockFp32: k_swiglu<kBlockFp32, BACK><<<grid, kWG, 0, st>>>(a); break;
-    case kBlockPow2: k_swiglu<kBlockPow2, BACK><<<grid, kWG, 0, st>>>(a); break;
-    default: k_swiglu<kNoPlanes, BACK><<<grid, kWG, 0, st>>>(a); break;
+    case kMxE4M3: k_swiglu<kMxE4M3, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kMxE5M2: k_swiglu<kMxE5M2, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kMxE2M1: k_swiglu<kMxE2M1, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kBlockFp32: k_swiglu<kBlockFp32, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    case kBlockPow2: k_swiglu<kBlockPow2, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    default: k_swiglu<kNoPlanes, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t st) { return a.dy ? run<true>(a, st) : run<false>(a, st); }
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t st)
+{
+    if (!a.dy)
+        return a.x_bf ? run<false, true, true>(a, st) : run<false, false, true>(a, st);
+    if (a.x_bf)
+        return a.dy_bf ? run<true, true, true>(a, st) : run<true, true, false>(a, st);
+    return a.dy_bf ? run<true, false, true>(a, st) : run<true, false, false>(a, st);
+}
 
 }  // namespace fq

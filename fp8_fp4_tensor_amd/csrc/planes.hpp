@@ -5,6 +5,8 @@
 // same fp32 values, bit for bit.
 #pragma once
 
+#include <type_traits>
+
 #include "codec.hpp"
 #include "launch.hpp"
 
@@ -90,26 +92,20 @@ __device__ __forceinline__ void row_plane8(const float* f, int64_t c, bool in, u
 }
 
 // ---------------------------------------------------------------- 128x128 tiles
-// A workgroup of 256 threads holds a tile; thread t has columns 8 (t % 16) ..
-// + 7 of rows 8 (t / 16) .. + 7. A row's 16 lanes read 256 contiguous bytes of
-// bf16, and a wave holds 32 rows, so that an MX block of either direction lies
-// within one wave.
+// A workgroup of 512 threads holds a tile; thread t has columns 4 (t % 32) ..
+// + 3 of rows 8 (t / 32) .. + 7: a row's 32 lanes read 256 contiguous bytes of
+// bf16, eight of them have an MX block of the row, and 32 values a thread leave
+// room for four waves a SIMD (64 values, two columns more of lanes, left two,
+// and the gated activation's gradient one: 623 us for 8192x14336).
 constexpr int kTileSide = 128;
+constexpr int kTileThreads = 512;
 
 struct TileLds {
-    uint8_t codes[kTileSide * 128];   // the codes of X^T
-    uint32_t scale[kTileSide * 4];    // a column's amaxes, by wave, then its scales
+    uint8_t codes[kTileSide * 128];     // the codes of X^T
+    uint32_t amax[8][kTileSide];        // of a wave's 16 rows
+    uint32_t scale[kTileSide];          // a column's scales: four E8M0 codes, or one fp32
+    uint32_t row_scale[kTileSide];      // a row's
 };
-
-// Where chunk ch (16 bytes) of column col lies. A wave writes eight bytes of
-// columns 8 apart at a time and reads whole rows of eight chunks: exchanging
-// odd and even columns in the upper half, and chunks by the column's group,
-// leaves no bank with more than its share in either.
-__device__ __forceinline__ int tile_at(int col, int ch)
-{
-    const int grp = col >> 3;
-    return (col ^ (grp >> 3 & 1)) * 128 + ((ch ^ (grp & 7)) << 4);
-}
 
 // A tile of a [R, C] tensor: its first row and column, and how many of its 128
 // rows and columns there are.
@@ -124,109 +120,210 @@ __device__ __forceinline__ TileSpan tile_span(int64_t tr, int64_t tc, int64_t R,
     return {r0, c0, (int)min((int64_t)kTileSide, R - r0), (int)min((int64_t)kTileSide, C - c0)};
 }
 
-// Rowwise planes of a thread's 8x8 values.
-template <int P>
-__device__ __forceinline__ void tile_rows(const float (&v)[8][8], const TileSpan& t, int64_t C, uint8_t* q, void* s)
-{
-    using T = PlaneTraits<P>;
-    const int c = (threadIdx.x & 15) * 8, r = (threadIdx.x >> 4) * 8;
-    const int64_t pitch = T::kFmt == kE2M1 ? C / 2 : C, scales = C / T::kBlock * (T::kMx ? 1 : 4);
-    uint8_t* to = q + (t.r0 + r) * pitch;
-    uint8_t* to_s = (uint8_t*)s + (t.r0 + r) * scales;
+// This thread's first column and row in a tile.
+__device__ __forceinline__ int tile_col() { return (threadIdx.x & 31) * 4; }
+__device__ __forceinline__ int tile_row() { return (threadIdx.x >> 5) * 8; }
+
+// Four consecutive values, as loaded and widened. Loads come first and all at
+// once; a row or column past the tile's last repeats it, so every address is
+// inside, and its values are not stored: blocks are whole or absent.
+template <bool BF>
+struct Four {
+    typename std::conditional<BF, u32x2, u32x4>::type raw;
+    __device__ __forceinline__ void load(const void* p, int64_t at)
+    {
+        if constexpr (BF)
+            raw = __builtin_nontemporal_load((const u32x2*)((const uint16_t*)p + at));
+        else
+            raw = __builtin_nontemporal_load((const u32x4*)((const float*)p + at));
+    }
+    __device__ __forceinline__ void widen(float* f) const
+    {
+        if constexpr (BF) {
+            f[0] = bf16_lo(raw[0]);
+            f[1] = bf16_hi(raw[0]);
+            f[2] = bf16_lo(raw[1]);
+            f[3] = bf16_hi(raw[1]);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        row_plane8<P>(v[i], t.c0 + c, c < t.cols && r + i < t.rows, to + i * pitch, to_s + i * scales);
+            for (int e = 0; e < 4; ++e)
+                f[e] = __uint_as_float(raw[e]);
+        }
+    }
+};
+
+// A thread's rows of a tile, one behind the other: a pointer that moves on by a
+// row, and stays at the tile's last. (Eight addresses at once would hold 16
+// registers for each tensor.)
+template <bool BF>
+struct TileRows {
+    const char* p;
+    int64_t step;
+    int left;  // rows behind this one
+    __device__ __forceinline__ TileRows(const void* base, const TileSpan& t, int64_t pitch, int64_t col)
+    {
+        constexpr int kBytes = BF ? 2 : 4;
+        const int r = min(tile_row(), t.rows - 1);
+        p = (const char*)base + ((t.r0 + r) * pitch + col) * kBytes;
+        step = pitch * kBytes;
+        left = t.rows - 1 - r;
+    }
+    __device__ __forceinline__ Four<BF> next()
+    {
+        Four<BF> f;
+        f.load(p, 0);
+        p += left > 0 ? step : 0;
+        --left;
+        return f;
+    }
+};
+
+__device__ __forceinline__ void store4v(void* p, bool bf, int64_t at, const float* f)
+{
+    if (bf)
+        *(u32x2*)((uint16_t*)p + at) = u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+    else
+        *(u32x4*)((float*)p + at) =
+            u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
 }
 
-// The maximum over the lanes 16 and 32 apart.
-__device__ __forceinline__ float max_rows_of_wave(float v)
+// Where chunk ch (16 bytes) of column col lies. A wave writes 16 bytes of
+// columns 4 apart at a time (two lanes, 8 rows each) and reads whole rows of
+// eight chunks: exchanging odd and even columns in every other eight of them,
+// and chunks by the column's group, leaves no bank with more than its share in
+// either.
+__device__ __forceinline__ int tile_at(int col, int ch)
 {
-    const uint32_t u = __float_as_uint(v);
-    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u, u, false, false));
-    const uint32_t w = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
-    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(w, w, false, false));
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    const int grp = col >> 2;
+    return (col ^ (grp >> 3 & 1)) * 128 + ((ch ^ (grp & 7)) << 4);
 }
 
-// The colwise plane of a tile: codes of X^T [C, R], whole lines of 128 bytes.
-// Values past the tile's rows are zeros. Every thread calls it; a second tile
-// may follow at once.
+// Planes of a tile's values: the rowwise one if q, the colwise one (codes of
+// X^T [C, R], whole lines of 128 bytes) if qt. Every thread calls it; a second
+// tile may follow at once.
 template <int P>
-__device__ __forceinline__ void tile_cols(const float (&v)[8][8], TileLds& lds, const TileSpan& t, int64_t R,
-                                          uint8_t* qt, void* st)
+__device__ __forceinline__ void tile_planes(const float (&v)[8][4], TileLds& lds, const TileSpan& t, int64_t R, int64_t C,
+                                            uint8_t* q, void* s, uint8_t* qt, void* st)
 {
     using T = PlaneTraits<P>;
-    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    float a[8];
+    constexpr bool kPacked = T::kFmt == kE2M1;
+    const int c = tile_col(), r = tile_row(), wave = threadIdx.x >> 6;
+    float a[4];
+    if (qt) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        a[e] = fabsf(v[0][e]);
+        for (int e = 0; e < 4; ++e) {
+            a[e] = fabsf(v[0][e]);
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
-            a[e] = fmaxf(a[e], fabsf(v[i][e]));
-        a[e] = max_rows_of_wave(a[e]);
+            for (int i = 1; i < 8; ++i)
+                a[e] = fmaxf(a[e], fabsf(v[i][e]));
+            // the wave's other eight rows
+            const uint32_t u = __float_as_uint(a[e]);
+            const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+            a[e] = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        }
     }
     lds_barrier();  // the previous tile has been read
-    if constexpr (!T::kMx) {
-        if ((rg & 3) == 0)
+    if (qt && (threadIdx.x & 32) == 0)
+        *(u32x4*)&lds.amax[wave][c] =
+            u32x4{__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3])};
+    if (q) {
+        const int64_t pitch = kPacked ? C / 2 : C;
+        uint8_t* to = q + (t.r0 + r) * pitch + (kPacked ? (t.c0 + c) / 2 : t.c0 + c);
+        const bool in = c < t.cols;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                lds.scale[wave * kTileSide + cg * 8 + e] = __float_as_uint(a[e]);
-        lds_barrier();
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                a[e] = fmaxf(a[e], __uint_as_float(lds.scale[w * kTileSide + cg * 8 + e]));
-        lds_barrier();
+        for (int i = 0; i < 8; ++i) {
+            float mult;
+            uint32_t stored;
+            block_scale<P>(max_lanes<T::kBlock / 4>(absmax<4>(v[i])), mult, stored);
+            if constexpr (kPacked) {
+                // two lanes' nibbles leave as one word
+                const float f[8] = {v[i][0], v[i][1], v[i][2], v[i][3], 0.0f, 0.0f, 0.0f, 0.0f};
+                const uint32_t half = enc8_e2m1(f, mult) & 0xFFFFu;
+                const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)half, kDppXor1, 0xF, 0xF, false);
+                if (in && r + i < t.rows && (threadIdx.x & 1) == 0)
+                    st4_stream(to + i * pitch, half | other << 16);
+            } else if (in && r + i < t.rows) {
+                st4_stream(to + i * pitch, enc4<T::kFmt>(v[i][0], v[i][1], v[i][2], v[i][3], mult));
+            }
+            if constexpr (T::kMx) {
+                if ((threadIdx.x & 7) == 0)
+                    ((uint8_t*)lds.row_scale)[(r + i) * 4 + (c >> 5)] = (uint8_t)stored;
+            } else if ((threadIdx.x & 31) == 0) {
+                lds.row_scale[r + i] = stored;
+            }
+        }
     }
+    lds_barrier();
+    if (q && threadIdx.x < t.rows) {
+        const int64_t per = C / T::kBlock;
+        const int64_t at = (t.r0 + threadIdx.x) * per + t.c0 / T::kBlock;
+        const uint32_t word = lds.row_scale[threadIdx.x];
+        if constexpr (!T::kMx) {
+            ((uint32_t*)s)[at] = word;
+        } else if (t.cols == kTileSide && (per & 3) == 0) {
+            *(uint32_t*)((uint8_t*)s + at) = word;
+        } else {
+            for (int j = 0; j < t.cols / 32; ++j)
+                ((uint8_t*)s)[at + j] = (uint8_t)(word >> 8 * j);
+        }
+    }
+    if (!qt)
+        return;
+    // the rows of a column's block: those of two waves, or of all
+    u32x4 m[T::kMx ? 2 : 8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int col = cg * 8 + e;
+    for (int w = 0; w < (T::kMx ? 2 : 8); ++w)
+        m[w] = *(const u32x4*)&lds.amax[T::kMx ? (wave & ~1) + w : w][c];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float all = __uint_as_float(m[0][e]);
+#pragma unroll
+        for (int w = 1; w < (T::kMx ? 2 : 8); ++w)
+            all = fmaxf(all, __uint_as_float(m[w][e]));
         float mult;
         uint32_t stored;
-        block_scale<P>(a[e], mult, stored);
-        if constexpr (T::kFmt == kE2M1) {
+        block_scale<P>(all, mult, stored);
+        const int col = c + e;
+        if constexpr (kPacked) {
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 f[i] = v[i][e];
-            *(uint32_t*)(lds.codes + tile_at(col, rg >> 2) + (rg & 3) * 4) = enc8_e2m1(f, mult);
+            *(uint32_t*)(lds.codes + tile_at(col, r >> 5) + (r >> 1 & 15)) = enc8_e2m1(f, mult);
         } else {
             u32x2 w;
             w[0] = enc4<T::kFmt>(v[0][e], v[1][e], v[2][e], v[3][e], mult);
             w[1] = enc4<T::kFmt>(v[4][e], v[5][e], v[6][e], v[7][e], mult);
-            *(u32x2*)(lds.codes + tile_at(col, rg >> 1) + (rg & 1) * 8) = w;
+            *(u32x2*)(lds.codes + tile_at(col, r >> 4) + (r & 8)) = w;
         }
         if constexpr (T::kMx) {
-            if ((rg & 3) == 0)
-                ((uint8_t*)lds.scale)[col * 4 + wave] = (uint8_t)stored;
-        } else if (rg == 0) {
+            if ((r & 31) == 0)
+                ((uint8_t*)lds.scale)[col * 4 + (r >> 5)] = (uint8_t)stored;
+        } else if (r == 0) {
             lds.scale[col] = stored;
         }
     }
     lds_barrier();
-    constexpr int kChunks = T::kFmt == kE2M1 ? 4 : 8;
-    const int64_t pitch = T::kFmt == kE2M1 ? R / 2 : R;
-    const int bytes = T::kFmt == kE2M1 ? t.rows / 2 : t.rows;
+    constexpr int kChunks = kPacked ? 4 : 8;
+    const int64_t pitch = kPacked ? R / 2 : R;
+    const int bytes = kPacked ? t.rows / 2 : t.rows;
 #pragma unroll
-    for (int k = 0; k < kChunks / 2; ++k) {
-        const int at = k * kWG + threadIdx.x, col = at / kChunks, ch = at % kChunks;
+    for (int k = 0; k < kChunks * kTileSide / kTileThreads; ++k) {
+        const int at = k * kTileThreads + threadIdx.x, col = at / kChunks, ch = at % kChunks;
         if (col < t.cols && ch * 16 < bytes)
-            st16_stream(qt + (t.c0 + col) * pitch + (T::kFmt == kE2M1 ? t.r0 / 2 : t.r0) + ch * 16,
-                        ld16(lds.codes + tile_at(col, ch)));
+            st16_stream(qt + (t.c0 + col) * pitch + (kPacked ? t.r0 / 2 : t.r0) + ch * 16, ld16(lds.codes + tile_at(col, ch)));
     }
-    const int col = threadIdx.x;
-    if (col < t.cols) {
-        if constexpr (T::kMx) {
-            uint8_t* to = (uint8_t*)st + (t.c0 + col) * (R / 32) + t.r0 / 32;
-            if (t.rows == kTileSide && (R / 32 & 3) == 0)
-                *(uint32_t*)to = lds.scale[col];
-            else
-                for (int j = 0; j < t.rows / 32; ++j)
-                    to[j] = ((const uint8_t*)lds.scale)[col * 4 + j];
+    if (threadIdx.x < t.cols) {
+        const int64_t per = R / T::kBlock;
+        const int64_t at = (t.c0 + threadIdx.x) * per + t.r0 / T::kBlock;
+        const uint32_t word = lds.scale[threadIdx.x];
+        if constexpr (!T::kMx) {
+            ((uint32_t*)st)[at] = word;
+        } else if (t.rows == kTileSide && (per & 3) == 0) {
+            *(uint32_t*)((uint8_t*)st + at) = word;
         } else {
-            ((uint32_t*)st)[(t.c0 + col) * (R / 128) + t.r0 / 128] = lds.scale[col];
+            for (int j = 0; j < t.rows / 32; ++j)
+                ((uint8_t*)st)[at + j] = (uint8_t)(word >> 8 * j);
         }
     }
 }
