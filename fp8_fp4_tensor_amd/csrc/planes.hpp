@@ -38,15 +38,30 @@ __device__ __forceinline__ void block_scale(float a, float& mult, uint32_t& stor
 }
 
 // ---------------------------------------------------------------- eight values of a row
-__device__ __forceinline__ void load8(const void* p, bool bf, int64_t at, float* f)
-{
-    if (bf) {
-        In<uint16_t>::unpack(ld16((const uint16_t*)p + at), f);
-    } else {
-        In<float>::unpack(ld16((const float*)p + at), f);
-        In<float>::unpack(ld16((const float*)p + at + 4), f + 4);
+// As loaded, and widened. A kernel whose types are a call's own loads all its
+// values before it widens the first: either is a branch that all lanes take
+// alike, but a load and its use within one branch would wait for each other.
+struct Eight {
+    u32x4 lo, hi;  // bf16: lo alone
+    __device__ __forceinline__ void load(const void* p, bool bf, int64_t at)
+    {
+        if (bf) {
+            lo = ld16((const uint16_t*)p + at);
+        } else {
+            lo = ld16((const float*)p + at);
+            hi = ld16((const float*)p + at + 4);
+        }
     }
-}
+    __device__ __forceinline__ void widen(bool bf, float* f) const
+    {
+        if (bf) {
+            In<uint16_t>::unpack(lo, f);
+        } else {
+            In<float>::unpack(lo, f);
+            In<float>::unpack(hi, f + 4);
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {

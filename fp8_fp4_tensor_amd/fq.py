@@ -665,19 +665,22 @@ class Planes(_Handle):
                              _empty=not given, _d=copy, _q=q, _dref=ctypes.byref(copy), _qref=ctypes.byref(q))
 
 
+_DTYPES = (torch.float32, torch.bfloat16)  # by fq_in_dtype
+
+
 def _rows2(t: torch.Tensor, rows: int, cols: int, dtype: int, what: str):
+    if t.dtype is not _DTYPES[dtype]:
+        raise TypeError(f"{what} is of the descriptor's type")
     if t.shape != (rows, cols) or not t.is_contiguous():
         raise ValueError(f"{what} is contiguous [{rows}, {cols}]")
-    if in_dtype_of(t) != dtype:
-        raise TypeError(f"{what} is of the descriptor's type")
 
 
 def _row_stride(t: torch.Tensor, rows: int, cols: int, dtype: int, what: str) -> int:
     """The row stride of a [rows, cols] tensor whose rows are each contiguous, 0 if the tensor is."""
+    if t.dtype is not _DTYPES[dtype]:
+        raise TypeError(f"{what} is of the descriptor's type")
     if t.shape != (rows, cols):
         raise ValueError(f"{what} is [{rows}, {cols}]")
-    if in_dtype_of(t) != dtype:
-        raise TypeError(f"{what} is of the descriptor's type")
     if t.is_contiguous():
         return 0
     step, one = t.stride()
@@ -687,7 +690,7 @@ def _row_stride(t: torch.Tensor, rows: int, cols: int, dtype: int, what: str) ->
 
 
 def _vector(t: Optional[torch.Tensor], n: int, dtype: int, what: str):
-    if t is not None and (t.numel() != n or not t.is_contiguous() or in_dtype_of(t) != dtype):
+    if t is not None and (t.dtype is not _DTYPES[dtype] or t.numel() != n or not t.is_contiguous()):
         raise TypeError(f"{what} is contiguous, of {n} values and of its type")
 
 
