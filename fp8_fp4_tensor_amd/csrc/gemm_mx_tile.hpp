@@ -192,6 +192,10 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
     constexpr int MT = T::kMT, NT = T::kNT, IA = T::kIA, IB = T::kIB, IS = T::kIS, P = T::kParts, G = 64 / S;
     constexpr bool kHalves = NS == 2;
     constexpr int H = NT / 2;
+    // Whether the scheduler is kept within a column tile. With widened operands beside a 64x128 tile's sums it would read
+    // more of them ahead than fit the registers (14336x4096x8192: 708 us, 761 without); without either it does better
+    // on its own (8192x14336x4096, 8-bit: 379 us, 389 with; 1003x7168x2048 21.3 and 21.8).
+    constexpr bool kFence = WIDE && (TM / WM) * (TN / WN) >= 64 * 128;
     static_assert(!kHalves || (NT % 2 == 0 && NT >= 4 && IB % 2 == 0), "two halves of a step");
     const GemmMxArgs& g = x.g;
     __shared__ typename T::Stage stage[NS];
@@ -445,7 +449,8 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
                         load_b(n, 0, 0);
                         products(t, [&](int u) { load_a(n, u); });
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (kFence)
+                        __builtin_amdgcn_sched_barrier(0);
                     if (t < H - 1) {
 #pragma unroll
                         for (int i = t * N1 / (H - 1); i < (t + 1) * N1 / (H - 1); ++i)

@@ -237,14 +237,16 @@ hipError_t by_cols(const NormArgs& a, hipStream_t st)
 template <int TPR, int NV, bool BF>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 512 ? 4 : 1) void k_rmsnorm_backward(NormBackArgs a)
 {
-    constexpr bool kAhead = TPR < 1024 || NV == 1;  // registers for a row ahead
+    // registers for a row ahead; otherwise dres and the weight come when they are needed
+    constexpr bool kAhead = TPR < 1024 || NV == 1;
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ float sums[2][TPR < 256 ? 4 : TPR / 64];
     const int sub = threadIdx.x / TPR;
     const bool h_bf = BF || a.h_bf, dy_bf = BF || a.dy_bf;
     const Columns<TPR, NV> c(a.cols);
     float w[NV][8], dw[NV][8];
-    load_weight(a.w, a.w_bf, c, w);
+    if (kAhead)
+        load_weight(a.w, a.w_bf, c, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 512 ? 4 : 1) void k_r
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             dy[i].load(a.dy, dy_bf, row * a.cols + c.at[i]);
-        if (a.dres)
+        if (kAhead && a.dres)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 past[i].load(a.dres, h_bf, row * a.cols + c.at[i]);
@@ -282,14 +284,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 512 ? 4 : 1) void k_r
         for (int i = 0; i < NV; ++i) {
             h[i].widen(h_bf, z[i]);
             dy[i].widen(dy_bf, g[i]);
-            if (a.dres) {
+            if (kAhead && a.dres)
                 past[i].widen(h_bf, d[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    d[i][e] = 0.0f;
-            }
         }
+        if (!kAhead)
+            load_weight(a.w, a.w_bf, c, w);
         // The next row's values come while this one's are worked on. dx may lie over any of this row's, which are
         // here, never over the next one's before those are.
         if (kAhead)
@@ -310,9 +309,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 512 ? 4 : 1) void k_r
         const float mean = sum_row<TPR>(dot, sums[turn]) / (float)a.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            if (!kAhead && a.dres) {
+                past[i].load(a.dres, h_bf, min(row, a.rows - 1) * a.cols + c.at[i]);
+                past[i].widen(h_bf, d[i]);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                d[i][e] = __builtin_fmaf(rstd, g[i][e] - z[i][e] * mean, d[i][e]);
+                d[i][e] = __builtin_fmaf(rstd, g[i][e] - z[i][e] * mean, a.dres ? d[i][e] : 0.0f);
             if (live && c.in[i])
                 store8(a.dx, h_bf, row * a.cols + c.at[i], d[i]);
         }

@@ -120,7 +120,7 @@ struct MxTileCost {
     double alone[4], full[4];
 };
 constexpr MxTileCost kMxTiles[] = {
-    {256, 256, 1, {1.50, 1.75, 1.50, 2.75}, {1.50, 1.75, 1.50, 2.75}},
+    {256, 256, 1, {1.60, 1.90, 1.56, 2.75}, {1.60, 1.90, 1.56, 2.75}},
     {128, 256, 1, {1.15, 1.41, 1.03, 1.60}, {1.15, 1.41, 1.03, 1.60}},
     {64, 128, 2, {0.50, 0.63, 0.47, 0.73}, {1.03, 1.18, 0.97, 1.22}},
     {64, 64, 3, {0.36, 0.43, 0.34, 0.56}, {0.98, 1.08, 0.90, 1.16}},
@@ -135,32 +135,48 @@ struct MxPlan {
     bool arranged = false;  // scales are laid out for the tiles first
 };
 
+// The ranking is plan_gemm_part's: steps times rounds of workgroups and the
+// bytes at 6.3 TB/s, the longer and a quarter of the other, plus the join of
+// shares. Measured both ways, what is chosen first (us; 8-bit both sides and
+// bf16 results where nothing is said):
+//   1x4096x4096        few rows 5.6, 64x64 in 8 shares 7.2
+//   16x8192x8192       64x64 in 4 shares 14.9, few rows 23.8
+//   16x18432x7168      64x128 in 3 shares 31.4, whole 39.7
+//   48x18432x7168      64x128 in 3 shares 37.4, whole 43.8; 4-bit 21.3 and 20.1
+//   256x4096x4096      64x64 14.7, 64x128 18.4
+//   1003x7168x2048     128x256 21.5, 256x256 27.1, 64x128 28.1
+//   512x4096x14336     128x256 in 4 shares 48.3, 256x256 in 6 50.6, 64x128 56.7
+//   4096x4096x4096     256x256 59.5, 128x256 72.6; 4-bit 42.9 and 50.1; fp32 103 and 120
+//   14336x4096x8192    fp32: three rounds of 256x256 and the rest on 128x256 700, all on 256x256 702, on 128x256 769
 inline MxPlan plan_gemm_mx_part(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bool bf)
 {
     MxPlan best;
     const int cost = a4 && b4 ? 1 : !bf ? 3 : a4 || b4 ? 2 : 0;
     const int64_t steps = ceil_div(k, a4 && b4 ? 256 : 128);
-    if (m <= 16 && n <= 8192)
-        return best;
     constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
     const double bytes = (double)m * (a4 ? k / 2 : k) + (double)n * (b4 ? k / 2 : k) + (double)(m + n) * k / 32 +
                          (double)m * n * (bf ? 2 : 4);
+    // few rows, and a workgroup of k_gemm_mx_few a CU or little of B: one launch and no LDS
+    // (12x9104x1152, 4-bit: 3.6 us, 64x64 4.7; 1x14336x4096, 4-bit B: 11.2, 64x64 in 2 shares 11.8)
+    if (m <= 16 && ((n <= 4096 && k <= 16384) || (double)n * (b4 ? k / 2 : k) <= 9e6))
+        return best;
     for (int t = 0; t < kMxTileKinds; ++t) {
         const MxTileCost& c = kMxTiles[t];
         const int64_t tiles = ceil_div(m, c.tm) * ceil_div(n, c.tn);
+        // one row of tiles takes B from memory and not from L2
+        const double one = c.alone[cost] * (c.per_cu > 1 && m <= c.tm ? 1.5 : 1.0), all = c.full[cost];
         for (int s : kSplits) {
             if (s > 1 && (steps / s < 2 || tiles >= 1024 || (double)s * m * n * 4 > 128e6))
                 break;
             const int64_t per_cu = ceil_div(tiles * s, kChipCus);  // workgroups of the busiest CU
             const int64_t rounds = per_cu / c.per_cu, left = per_cu % c.per_cu;
-            const double one = c.alone[cost], all = c.full[cost];
             double step = rounds * all;
             if (left)
-                step += c.per_cu == 1 ? one : one + (all - one) * (left - 1) / (c.per_cu - 1);
-            const double work = ceil_div(steps, s) * step, read = bytes / 5e6;
+                step += c.per_cu == 1 || one > all ? one : one + (all - one) * (left - 1) / (c.per_cu - 1);
+            const double work = ceil_div(steps, s) * step, read = bytes / 6.3e6;
             double us = work > read ? work + read / 4 : read + work / 4;  // overlapped, but not wholly
             if (s > 1)
-                us += 3.0 + (double)s * m * n * 8 / 6e6;
+                us += 4.5 + (double)s * m * n * 8 / 6e6;
             if (best.kind < 0 || us < best.us) {
                 best.kind = t;
                 best.splits = s;
@@ -181,19 +197,28 @@ inline MxPlan plan_gemm_mx(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bo
         if (main > 0 && main < m) {
             MxPlan rest = plan_gemm_mx_part(m - main, n, k, a4, b4, bf);
             rest.us += plan_gemm_mx_part(main, n, k, a4, b4, bf).us + 2.0;
-            if (rest.kind >= 0 && rest.us < best.us) {
+            if (rest.kind >= 0 && rest.us < best.us) {  // not k_gemm_mx_few: it takes no laid out scales
                 best = rest;
                 best.main = main;
             }
         }
     }
-    // A row's scales as the plane has them are four (or eight) bytes a step, a
-    // line of memory each: half (for 4-bit sides all) as many lines again as the
-    // operands. Words laid out by rows first cost a launch.
+    // Scales that a 256x256 tile takes from a plane are a line of memory for
+    // each row, word and step, half as many again as the operands (with 4-bit
+    // sides as many again). Laid out by rows first they are 1 KB in a piece,
+    // which saves about 0.18 us a step (0.3, and 0.08 with one 4-bit side) and
+    // costs a launch of 6 us or more; with widened operands it saves nothing.
+    //   8192x14336x4096  8-bit 382 us, 452 without; 4-bit 261, 294; one of each 368, 387
+    //   2048x14336x4096  8-bit 105, 109
+    //   4096x14336x4096  8-bit 211, 252; 4-bit 133, 148
+    //   18432x7168x2048  4-bit 169, 161 without: eight steps, and results that take as long to write
+    // A plane whose rows of scales are no whole words needs it whatever the size.
+    const int cost = a4 && b4 ? 1 : !bf ? 3 : a4 || b4 ? 2 : 0;
+    constexpr double kSaves[] = {0.18, 0.30, 0.08, 0.0};
     const int64_t steps = ceil_div(k, a4 && b4 ? 256 : 128);
     const int64_t rounds = ceil_div(ceil_div(best.main ? best.main : m, 256) * across, kChipCus);
-    const bool wide = !bf && !(a4 && b4);
-    best.arranged = best.kind >= 0 && (k % 128 != 0 || (!wide && (best.kind == 0 || best.main) && rounds * steps >= 48));
+    const bool large = best.main || (best.kind == 0 && best.splits == 1);
+    best.arranged = best.kind >= 0 && (k % 128 != 0 || (large && steps >= 12 && kSaves[cost] * rounds * steps > 10.0));
     return best;
 }
 
