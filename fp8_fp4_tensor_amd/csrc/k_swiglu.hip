@@ -28,6 +28,79 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& rest)
     rest = g < 0.0f ? q : u;
 }
 
+// One value: y, or with BACK dgate and dup.
+template <bool BACK>
+__device__ __forceinline__ void gated(float gate, float up, float dy, float& first, float& second)
+{
+    float s, rest;
+    sigmoid(gate, s, rest);
+    if constexpr (BACK) {
+        const float ds = dy * s;
+        first = ds * up * __builtin_fmaf(gate, rest, 1.0f);
+        second = ds * gate;
+    } else {
+        first = gate * s * up;
+    }
+}
+
+// ---------------------------------------------------------------- rows alone
+// Without colwise planes nothing is shared but a row's blocks: a thread takes
+// eight columns of a row, and there are as many threads as that gives
+// (48x18432: 3.1 us, in 128x128 tiles 5.6; the gradient of 896x7168 in blocks of 128: 10.7 and 20.4).
+template <int P, bool BACK>
+__global__ __launch_bounds__(kWG) void k_swiglu_rows(SwigluArgs a)
+{
+    const int64_t c = ((int64_t)blockIdx.x * kWG + threadIdx.x) * 8;
+    const bool in = c < a.cols;
+    const int64_t at = in ? c : a.cols - 8;  // past the last columns: the last ones again, not stored
+    const int64_t C = BACK ? 2 * a.cols : a.cols;
+    using T = PlaneTraits<P>;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        Eight gate, up, dy;
+        gate.load(a.x, a.x_bf, row * a.x_stride + at);
+        up.load(a.x, a.x_bf, row * a.x_stride + a.cols + at);
+        if constexpr (BACK)
+            dy.load(a.dy, a.dy_bf, row * a.cols + at);
+        float g[8], u[8], d[8], first[8], second[8];
+        gate.widen(a.x_bf, g);
+        up.widen(a.x_bf, u);
+        if constexpr (BACK)
+            dy.widen(a.dy_bf, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            gated<BACK>(g[e], u[e], BACK ? d[e] : 0.0f, first[e], second[e]);
+        if (a.y && in) {
+            store8(a.y, a.y_bf, row * C + c, first);
+            if constexpr (BACK)
+                store8(a.y, a.y_bf, row * C + a.cols + c, second);
+        }
+        if constexpr (P != kNoPlanes) {
+            uint8_t* q = a.q + row * (T::kFmt == kE2M1 ? C / 2 : C);
+            uint8_t* s = (uint8_t*)a.s + row * (C / T::kBlock) * (T::kMx ? 1 : 4);
+            row_plane8<P>(first, c, in, q, s);
+            if constexpr (BACK)
+                row_plane8<P>(second, c + a.cols, in, q, s);
+        }
+    }
+}
+
+template <bool BACK>
+hipError_t by_rows(const SwigluArgs& a, hipStream_t st)
+{
+    // a grid's dimension has less than 2^32 threads, and 65536 workgroups in its second
+    const dim3 grid((unsigned)cdiv(a.cols, 8 * kWG), (unsigned)std::min<int64_t>(a.rows, 65535));
+    switch (a.q ? a.kind : (int)kNoPlanes) {
+    case kMxE4M3: k_swiglu_rows<kMxE4M3, BACK><<<grid, kWG, 0, st>>>(a); break;
+    case kMxE5M2: k_swiglu_rows<kMxE5M2, BACK><<<grid, kWG, 0, st>>>(a); break;
+    case kMxE2M1: k_swiglu_rows<kMxE2M1, BACK><<<grid, kWG, 0, st>>>(a); break;
+    case kBlockFp32: k_swiglu_rows<kBlockFp32, BACK><<<grid, kWG, 0, st>>>(a); break;
+    case kBlockPow2: k_swiglu_rows<kBlockPow2, BACK><<<grid, kWG, 0, st>>>(a); break;
+    default: k_swiglu_rows<kNoPlanes, BACK><<<grid, kWG, 0, st>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- tiles
 // High-precision copy and planes of a tile of [R, C].
 template <int P>
 __device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][4], TileLds& lds, const TileSpan& t,
@@ -40,11 +113,10 @@ __device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][4]
             if (c < t.cols && r + i < t.rows)
                 store4v(a.y, a.y_bf, (t.r0 + r + i) * C + t.c0 + c, v[i]);
     }
-    if constexpr (P != kNoPlanes)
-        tile_planes<P>(v, lds, t, R, C, a.q, a.s, a.qt, a.st);
+    tile_planes<P>(v, lds, t, R, C, a.q, a.s, a.qt, a.st);
 }
 
-// A 128x128 tile of gate, of up and with BACK of dy a workgroup.
+// A 128x128 tile of gate, of up and with BACK of dy a workgroup, for colwise planes.
 template <int P, bool BACK, bool XBF, bool DBF>
 __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
 {
@@ -77,16 +149,9 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
                 dy[i].widen(d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float s, rest;
-                sigmoid(g[e], s, rest);
-                if constexpr (BACK) {
-                    const float ds = d[e] * s;
-                    v[i][e] = ds * u[e] * __builtin_fmaf(g[e], rest, 1.0f);
-                    w[i][e] = ds * g[e];
+                gated<BACK>(g[e], u[e], BACK ? d[e] : 0.0f, v[i][e], w[BACK ? i : 0][e]);
+                if constexpr (BACK)
                     asm volatile("" : "+v"(w[i][e]));  // here: the compiler would keep both factors until its use
-                } else {
-                    v[i][e] = g[e] * s * u[e];
-                }
             }
             // rows one after the other: all at once would hold their intermediate values too
             __builtin_amdgcn_sched_barrier(0);
@@ -106,13 +171,12 @@ hipError_t run(const SwigluArgs& a, hipStream_t st)
 {
     const int64_t tiles = cdiv(a.rows, kTileSide) * cdiv(a.cols, kTileSide);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, 1 << 20);
-    switch (a.q || a.qt ? a.kind : (int)kNoPlanes) {
+    switch (a.kind) {
     case kMxE4M3: k_swiglu<kMxE4M3, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
     case kMxE5M2: k_swiglu<kMxE5M2, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
     case kMxE2M1: k_swiglu<kMxE2M1, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
     case kBlockFp32: k_swiglu<kBlockFp32, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
-    case kBlockPow2: k_swiglu<kBlockPow2, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
-    default: k_swiglu<kNoPlanes, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
+    default: k_swiglu<kBlockPow2, BACK, XBF, DBF><<<grid, kTileThreads, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }
@@ -121,6 +185,8 @@ hipError_t run(const SwigluArgs& a, hipStream_t st)
 
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t st)
 {
+    if (!a.qt)
+        return a.dy ? by_rows<true>(a, st) : by_rows<false>(a, st);
     if (!a.dy)
         return a.x_bf ? run<false, true, true>(a, st) : run<false, false, true>(a, st);
     if (a.x_bf)
