@@ -593,13 +593,15 @@ fq_status fq_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, const
  * The result is rounded once to out_dtype from fp32 sums. With 8-bit elements
  * on both sides and bf16 outputs the matrix instruction keeps each product to
  * about 2^-12 of the largest of its 128 (1.5e-5 of the result in the mean
- * square, against the output's rounding of 2^-9). fp32 outputs have products and sums in fp32
- * throughout; there a value below 2^-126 in magnitude may count as zero.
+ * square, against 2^-9 for the output's rounding). fp32 outputs have products
+ * and sums in fp32 throughout; there a value below 2^-126 in magnitude may
+ * count as zero.
  *   accumulate   1: C += the product (FQ_IN_F32 only), 0: C = the product.
  *   k % 32 == 0; m*k, n*k and m*n at most 2^36, k at most 2^22, m and n at most 2^28.
  * k = 0 gives zeros (or leaves C with accumulate); m = 0 or n = 0 does nothing.
- * Codes must be finite and scale codes below 255. The result does not depend
- * on the run: no atomics, sums in a fixed order.
+ * A NaN code or a scale code of 255 makes the results that it takes part in
+ * NaN; E5M2's infinities count as what they are. The result does not depend on
+ * the run: no atomics, sums in a fixed order.
  */
 typedef struct {
     int64_t m, n, k;
