@@ -1023,6 +1023,9 @@ fq_status fq_rmsnorm(const fq_rmsnorm_desc* d, const fq_desc* planes, const void
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(rstd, 4) ||
         !aligned(y, 16))
         return FQ_E_ALIGN;
+    // h over x: each element has to lie where it was read
+    if ((h && h == x && (d->h_dtype != d->x_dtype || a.x_stride != d->cols)) || (y && (y == x || y == residual || y == h)))
+        return FQ_E_INVALID;
     a.rows = d->rows;
     a.cols = d->cols;
     a.x = x;
@@ -1071,6 +1074,8 @@ fq_status fq_rmsnorm_backward(const fq_rmsnorm_desc* d, const void* h, const flo
         if (!aligned(ws, 16))
             return FQ_E_ALIGN;
     }
+    if (d->rows > 0 && dx == dy && d->h_dtype != d->y_dtype)
+        return FQ_E_INVALID;
     NormBackArgs a;
     a.rows = d->rows;
     a.cols = d->cols;
@@ -1095,7 +1100,7 @@ static fq_status swiglu_args(const fq_swiglu_desc* d, const fq_desc* planes, con
 {
     if (!d || d->rows < 0 || d->cols < 0 || !in_dtype(d->x_dtype) || !in_dtype(d->y_dtype))
         return FQ_E_INVALID;
-    if (d->cols % 8 || (d->cols > 0 && d->rows > kMaxElems / 2 / d->cols))
+    if (d->cols % 8 || d->cols > (int64_t(1) << 28) || (d->cols > 0 && d->rows > kMaxElems / 2 / d->cols))
         return FQ_E_SHAPE;
     a.x_stride = d->x_stride;
     fq_status s = check_stride(a.x_stride, 2 * d->cols, d->rows, d->x_dtype);
@@ -1129,6 +1134,8 @@ fq_status fq_swiglu(const fq_swiglu_desc* d, const fq_desc* planes, const void* 
         return FQ_E_INVALID;
     if (!aligned(x, 16) || !aligned(y, 16))
         return FQ_E_ALIGN;
+    if (x == y)
+        return FQ_E_INVALID;
     a.x = x;
     a.y = y;
     a.y_bf = d->y_dtype == FQ_IN_BF16;
@@ -1150,6 +1157,8 @@ fq_status fq_swiglu_backward(const fq_swiglu_desc* d, const fq_desc* planes, con
         return FQ_E_INVALID;
     if (!aligned(x, 16) || !aligned(dy, 16) || !aligned(dx, 16))
         return FQ_E_ALIGN;
+    if (dx && (dx == dy || (dx == x && a.x_stride != 2 * d->cols)))
+        return FQ_E_INVALID;
     a.x = x;
     a.dy = dy;
     a.y = dx;

@@ -643,8 +643,8 @@ fq_status fq_gemm_mx(const fq_gemm_mx_desc *desc, const fq_plane *a, const fq_pl
  * format), or FQ_BLOCK_FP32 with 1x128 tiles (either scale mode); rounding
  * to nearest even, no transform; rows and cols those of the norm; rowwise, colwise or
  * both. in_dtype, seed, offset and rht_signs are not read.
- * At least one of y and the planes is asked for. The sum of a row's squares
- * must be finite in fp32.
+ * At least one of y and the planes is asked for; both lie apart from all other
+ * tensors. The sum of a row's squares must be finite in fp32.
  */
 typedef struct {
     int64_t rows, cols;
@@ -686,7 +686,8 @@ fq_status fq_rmsnorm_backward(const fq_rmsnorm_desc *desc, const void *h, const 
  *             2 * cols): a row's gate, then its up
  *   y         [rows, cols] of y_dtype, or NULL
  *   planes, out   as for fq_rmsnorm, of [rows, cols]
- *   cols % 8 == 0, 2*rows*cols <= 2^36; x_stride a multiple of 8 (bf16) or 4.
+ *   cols % 8 == 0, cols <= 2^28, 2*rows*cols <= 2^36; x_stride a multiple of 8
+ *   (bf16) or 4. x finite.
  */
 typedef struct {
     int64_t rows, cols;
@@ -702,7 +703,9 @@ fq_status fq_swiglu(const fq_swiglu_desc *desc, const fq_desc *planes, const voi
  * Its gradient. With s = 1 / (1 + exp(-gate)),
  *   dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s
  *   dy    [rows, cols] of y_dtype
- *   dx    [rows, 2 * cols] of x_dtype, contiguous: dgate, then dup; or NULL
+ *   dx    [rows, 2 * cols] of x_dtype, contiguous: dgate, then dup; or NULL. It
+ *         may be x, if that is contiguous: each element is read before it is
+ *         written.
  *   planes, out   of the fp32 dx, [rows, 2 * cols] (planes->cols = 2 * cols,
  *                 cols a multiple of the block)
  */

@@ -342,3 +342,28 @@ def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
         fq.fq_swiglu(fq.swiglu_desc(4, 64), t(4, 128), t(4, 64), stream=Stream)
     with pytest.raises(ValueError, match="current"):
         fq.fq_rmsnorm(fq.rmsnorm_desc(4, 64), t(4, 64), t(64, dtype=torch.float32), y=t(4, 64), stream=Stream)
+
+
+def test_outputs_over_inputs(L):
+    """What a kernel would read after it is written is refused; results over what is read first are not (they fail later
+    or run, so only the refusals are seen here)."""
+    Q, R, S = P + 4096, P + 8192, P + 12288
+    for d, kw in ((ndesc(h_dtype=F32), dict(x=P, res=Q, h=P, y=R)), (ndesc(x_stride=512), dict(x=P, res=Q, h=P, y=R)),
+                  (ndesc(), dict(x=P, y=P)), (ndesc(), dict(x=P, res=Q, h=R, y=R)), (ndesc(), dict(x=P, res=Q, h=R, y=Q))):
+        assert norm(L, d, w=S, **kw) == fq.FQ_E_INVALID, kw
+    assert back(L, ndesc(h_dtype=F32), h=P, dy=Q, dx=Q, dw=None) == fq.FQ_E_INVALID
+    d, s = fq.FqSwigluDesc(64, 256, BF, BF, 0), fq.FqSwigluDesc(64, 256, BF, BF, 1024)
+    assert L.fq_swiglu(ref(d), None, P, P, None, None) == fq.FQ_E_INVALID
+    assert L.fq_swiglu_backward(ref(d), None, P, Q, Q, None, None) == fq.FQ_E_INVALID
+    assert L.fq_swiglu_backward(ref(s), None, P, Q, P, None, None) == fq.FQ_E_INVALID
+
+
+def test_largest_shapes(L):
+    """Just past each limit, and sizes whose products would overflow 64 bits."""
+    sw = lambda r, c: L.fq_swiglu(ref(fq.FqSwigluDesc(r, c, BF, BF, 0)), None, P, P + 4096, None, None)
+    assert sw(1, (1 << 28) + 8) == sw(0, 1 << 62) == sw(1 << 62, 8) == sw((1 << 7) + 1, 1 << 28) == fq.FQ_E_SHAPE
+    mx = lambda m, n, k: L.fq_gemm_mx_workspace(ref(fq.gemm_mx_desc(m, n, k)), None)
+    assert mx((1 << 28) + 1, 1, 32) == mx(1, (1 << 28) + 1, 32) == mx(1, 1, (1 << 22) + 32) == fq.FQ_E_SHAPE
+    assert mx(1 << 20, 1 << 17, 32) == mx(1 << 62, 1 << 62, 32) == fq.FQ_E_SHAPE
+    assert mx(1 << 28, 1 << 8, 32) == mx(1, 1 << 28, 256) == mx(1 << 14, 1 << 14, 1 << 22) == fq.FQ_OK
+    assert norm(L, ndesc(rows=1 << 62)) == norm(L, ndesc(rows=(1 << 28) + 1)) == fq.FQ_E_SHAPE
