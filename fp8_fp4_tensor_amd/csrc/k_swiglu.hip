@@ -4,13 +4,22 @@
 //   dgate = dy up s (1 + gate (1 - s)),   dup = dy gate s.
 //
 // Nothing crosses rows or columns but the blocks' scales, so a 128x128 tile is
-// read once and leaves as rowwise and colwise planes. The exponential is that
-// of -|g| in base 2, which neither overflows nor cancels: with e = exp(-|g|)
-// and q = 1 / (1 + e), s and 1 - s are q and e q, the larger one for the sign
-// of g that has it. The hardware's base-2 exponential and reciprocal are off
-// by a unit in the last place each, the exponent's own rounding by 2^-24 |g|
-// log2(e): together below 2^-18 for |g| < 40. Below -87, exp(-|g|) is no
-// normal number and counts as zero.
+// read once and leaves as rowwise and colwise planes. With e = exp(-g), s is
+// 1 / (1 + e) and 1 - s is e s, neither of which cancels. The hardware's base-2
+// exponential and its reciprocal are off by a unit in the last place each; the
+// exponent's rounding, which would add 2^-24 |g| log2(e), is taken back to first
+// order, and the reciprocal refined once: s is off by 5e-8 in the mean square,
+// 9e-8 without, and codes differ that much more seldom from those of the exact
+// result (8192x14336: 143 us, 142.5 without). Where exp(-|g|) is no normal number
+// it counts as zero: gates beyond 87.
+//
+// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 143 us,
+// 5.0 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 259 us, 4.6 TB/s,
+// whose scales, a word for each row and column of a tile, add 57 MB of partial
+// lines. Other orders of the tiles (runs of each XCD's own, bands of 2 to 64
+// rows of tiles) bring those together, but move the times by 10% either way with the
+// pitch of the rows (bands of 16: 135 and 231 us here, but 94 and 157 for
+// 8192x8192 where the plain order takes 84 and 146).
 #include <algorithm>
 
 #include "launch.hpp"
@@ -19,13 +28,15 @@
 namespace fq {
 namespace {
 
-// s = 1 / (1 + exp(-g)) and 1 - s
+// s = 1 / (1 + exp(-g)) and 1 - s. Gates beyond what is asked for here have s = 0 or 1 - s = 0 already.
 __device__ __forceinline__ void sigmoid(float g, float& s, float& rest)
 {
-    const float e = __builtin_amdgcn_exp2f(fabsf(g) * -1.44269504f);
-    const float q = __builtin_amdgcn_rcpf(1.0f + e), u = e * q;
-    s = g < 0.0f ? u : q;
-    rest = g < 0.0f ? q : u;
+    const float a = __builtin_amdgcn_fmed3f(g, -88.5f, 128.0f), t = a * -1.44269504f;
+    const float p = __builtin_amdgcn_exp2f(t);
+    const float e = __builtin_fmaf(p, __builtin_fmaf(a, -1.44269504f, -t) * 0.693147181f, p);
+    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+    s = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+    rest = e * s;
 }
 
 // One value: y, or with BACK dgate and dup.
@@ -116,49 +127,70 @@ __device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][4]
     tile_planes<P>(v, lds, t, R, C, a.q, a.s, a.qt, a.st);
 }
 
+// Rows of a thread's dup that wait in LDS while dgate leaves.
+constexpr int kKept = 6;
+
 // A 128x128 tile of gate, of up and with BACK of dy a workgroup, for colwise planes.
 template <int P, bool BACK, bool XBF, bool DBF>
 __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
 {
     __shared__ __align__(16) TileLds lds;
+    __shared__ u32x4 kept[BACK ? kKept : 1][kTileThreads];
     const int64_t across = cdiv(a.cols, kTileSide), tiles = across * cdiv(a.rows, kTileSide);
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int64_t tr, tc;
         tile_coords(t, across, tr, tc);
         TileSpan span = tile_span(tr, tc, a.rows, a.cols);
         const int64_t c = span.c0 + min(tile_col(), span.cols - 4);
-        Four<XBF> gate[8], up[8];
-        Four<DBF> dy[BACK ? 8 : 1];
         TileRows<XBF> gates(a.x, span, a.x_stride, c), ups(a.x, span, a.x_stride, a.cols + c);
         TileRows<DBF> dys(BACK ? a.dy : a.x, span, a.cols, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            gate[i] = gates.next();
-            up[i] = ups.next();
-            if constexpr (BACK)
-                dy[i] = dys.next();
-        }
-        __builtin_amdgcn_sched_barrier(0);
         float v[8][4], w[BACK ? 8 : 1][4];
+        // all eight rows' loads at once; with fp32 operands of the gradient, which would not fit the registers, four's
+        constexpr int kAt = BACK && !XBF ? 4 : 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float g[4], u[4], d[4];
-            gate[i].widen(g);
-            up[i].widen(u);
-            if constexpr (BACK)
-                dy[i].widen(d);
+        for (int i0 = 0; i0 < 8; i0 += kAt) {
+            Four<XBF> gate[kAt], up[kAt];
+            Four<DBF> dy[BACK ? kAt : 1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                gated<BACK>(g[e], u[e], BACK ? d[e] : 0.0f, v[i][e], w[BACK ? i : 0][e]);
+            for (int i = 0; i < kAt; ++i) {
+                gate[i] = gates.next();
+                up[i] = ups.next();
                 if constexpr (BACK)
-                    asm volatile("" : "+v"(w[i][e]));  // here: the compiler would keep both factors until its use
+                    dy[i] = dys.next();
             }
-            // rows one after the other: all at once would hold their intermediate values too
             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = i0; i < i0 + kAt; ++i) {
+                float g[4], u[4], d[4];
+                gate[i - i0].widen(g);
+                up[i - i0].widen(u);
+                if constexpr (BACK)
+                    dy[i - i0].widen(d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    gated<BACK>(g[e], u[e], BACK ? d[e] : 0.0f, v[i][e], w[BACK ? i : 0][e]);
+                    if constexpr (BACK)
+                        asm volatile("" : "+v"(w[i][e]));  // here: the compiler would keep both factors until its use
+                }
+                if (BACK && i < kKept) {
+                    const float* d = w[BACK ? i : 0];
+                    kept[i][threadIdx.x] =
+                        u32x4{__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3])};
+                }
+                // rows one after the other: all at once would hold their intermediate values too
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if constexpr (BACK) {
             emit<P>(a, v, lds, span, a.rows, 2 * a.cols);
             span.c0 += a.cols;
+#pragma unroll
+            for (int i = 0; i < kKept; ++i) {
+                const u32x4 d = kept[i][threadIdx.x];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[i][e] = __uint_as_float(d[e]);
+            }
             emit<P>(a, w, lds, span, a.rows, 2 * a.cols);
         } else {
             emit<P>(a, v, lds, span, a.rows, a.cols);
