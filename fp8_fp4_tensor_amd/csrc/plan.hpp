@@ -206,19 +206,21 @@ inline MxPlan plan_gemm_mx(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bo
     // Scales that a 256x256 tile takes from a plane are a line of memory for
     // each row, word and step, half as many again as the operands (with 4-bit
     // sides as many again). Laid out by rows first they are 1 KB in a piece,
-    // which saves about 0.18 us a step (0.3, and 0.08 with one 4-bit side) and
-    // costs a launch of 6 us or more; with widened operands it saves nothing.
+    // which saves about 0.18 us a step (0.3, and 0.115 with one 4-bit side) and
+    // costs a launch of 5 us or more; with widened operands it saves nothing.
     //   8192x14336x4096  8-bit 382 us, 452 without; 4-bit 261, 294; one of each 368, 387
-    //   2048x14336x4096  8-bit 105, 109
     //   4096x14336x4096  8-bit 211, 252; 4-bit 133, 148
+    //   4096x4096x7168   8-bit 95.0, 96.3;  4096x4096x5120  73.7, 73.5;  4096x4096x4096  64.0, 61.3
+    //   8192x4096x4096   4-bit 79.6, 80.9;  4096x4096x4096  45.0, 42.6
+    //   4096x4096x14336  one of each 164, 172;  8192x8192x2048  121.9, 120.7
     //   18432x7168x2048  4-bit 169, 161 without: eight steps, and results that take as long to write
     // A plane whose rows of scales are no whole words needs it whatever the size.
     const int cost = a4 && b4 ? 1 : !bf ? 3 : a4 || b4 ? 2 : 0;
-    constexpr double kSaves[] = {0.18, 0.30, 0.08, 0.0};
+    constexpr double kSaves[] = {0.18, 0.30, 0.115, 0.0};
     const int64_t steps = ceil_div(k, a4 && b4 ? 256 : 128);
     const int64_t rounds = ceil_div(ceil_div(best.main ? best.main : m, 256) * across, kChipCus);
     const bool large = best.main || (best.kind == 0 && best.splits == 1);
-    best.arranged = best.kind >= 0 && (k % 128 != 0 || (large && steps >= 12 && kSaves[cost] * rounds * steps > 10.0));
+    best.arranged = best.kind >= 0 && (k % 128 != 0 || (large && steps >= 12 && kSaves[cost] * rounds * steps > 7.5));
     return best;
 }
 
