@@ -13,13 +13,13 @@
 // result (8192x14336: 143 us, 142.5 without). Where exp(-|g|) is no normal number
 // it counts as zero: gates beyond 87.
 //
-// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 143 us,
-// 5.0 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 259 us, 4.6 TB/s,
-// whose scales, a word for each row and column of a tile, add 57 MB of partial
-// lines. Other orders of the tiles (runs of each XCD's own, bands of 2 to 64
-// rows of tiles) bring those together, but move the times by 10% either way with the
-// pitch of the rows (bands of 16: 135 and 231 us here, but 94 and 157 for
-// 8192x8192 where the plain order takes 84 and 146).
+// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 136 us,
+// 5.2 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 248 us, 4.8 TB/s.
+// The scales are a word for each row and column of a tile, so that planes and
+// scales of 485 MB are 533 MB of lines in the gradient. Giving each XCD an
+// eighth of all tiles, in bands of 2 to 64 rows of tiles, would bring more of
+// them together, but moves the times by 10% either way with the pitch of the rows (bands
+// of 16: 135 and 231 us here, 94 and 157 for 8192x8192 where runs take 80 and 137).
 #include <algorithm>
 
 #include "launch.hpp"
@@ -130,6 +130,18 @@ __device__ __forceinline__ void emit(const SwigluArgs& a, const float (&v)[8][4]
 // Rows of a thread's dup that wait in LDS while dgate leaves.
 constexpr int kKept = 6;
 
+// The tile of turn t. Consecutive workgroups go to the eight XCDs in turn; a
+// run of eight neighbouring tiles goes to one of them instead, whose L2 then
+// has whole pieces of the rows and of their scales. The order of the whole stays
+// the rows' own. (8192x14336 139 and 244 us, 146 and 254 without; 8192x8192 80
+// and 137, 83 and 146; runs of 2, 4, 16 and 32 in between or the same.)
+__device__ __forceinline__ int64_t tile_in_turn(int64_t t, int64_t tiles)
+{
+    constexpr uint32_t kRun = 8;
+    const uint32_t u = (uint32_t)t, first = u / (8 * kRun) * (8 * kRun);
+    return first + 8 * kRun <= (uint32_t)tiles ? first + u % 8 * kRun + (u - first) / 8 : u;
+}
+
 // A 128x128 tile of gate, of up and with BACK of dy a workgroup, for colwise planes.
 template <int P, bool BACK, bool XBF, bool DBF>
 __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
@@ -139,7 +151,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_swiglu(SwigluArgs a)
     const int64_t across = cdiv(a.cols, kTileSide), tiles = across * cdiv(a.rows, kTileSide);
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         int64_t tr, tc;
-        tile_coords(t, across, tr, tc);
+        tile_coords(tile_in_turn(t, tiles), across, tr, tc);
         TileSpan span = tile_span(tr, tc, a.rows, a.cols);
         const int64_t c = span.c0 + min(tile_col(), span.cols - 4);
         TileRows<XBF> gates(a.x, span, a.x_stride, c), ups(a.x, span, a.x_stride, a.cols + c);
