@@ -10,6 +10,13 @@
 // LDS in lane order, so it is the lane's source address that carries the
 // permutation. Chunks past k read beyond the buffer's declared end, which
 // gives zeros.
+//
+// Matrix instructions bound large products, and the clock that they leave
+// (1.8 to 1.9 GHz): 8192x14336x4096 4-bit 267 us (3.6 PFLOP/s), 8-bit 382 (2.5),
+// 8192x4096x14336 8-bit 356 (2.7; the library's unscaled 8-bit product of 8192^3
+// reaches 2.68), 4-bit 211 (4.6). Of the 267 us 50 are stores: all workgroups end their
+// tiles together. Storing a column tile just before its first product of the
+// next tile only moves that wait (282 us).
 #pragma once
 
 #include "gemm_mx.hpp"

@@ -7,6 +7,10 @@
 // instruction applies the scales, so a product is nothing but operands in and
 // sums out.
 //
+// A few rows take a kernel without LDS tiles or a second launch (1x4096x4096,
+// 8-bit times 4-bit: 4.2 us, two latencies of memory and a launch), others tiles
+// (gemm_mx_tile.hpp).
+//
 // Operand order: B's rows are the instruction's rows and A's rows its columns,
 // so a lane holds one row i of C and four consecutive columns j.
 #include "gemm_mx.hpp"

@@ -10,11 +10,11 @@
 // exponent's rounding, which would add 2^-24 |g| log2(e), is taken back to first
 // order, and the reciprocal refined once: s is off by 5e-8 in the mean square,
 // 9e-8 without, and codes differ that much more seldom from those of the exact
-// result (8192x14336: 143 us, 142.5 without). Where exp(-|g|) is no normal number
+// result (8192x14336: a microsecond). Where exp(-|g|) is no normal number
 // it counts as zero: gates beyond 87.
 //
-// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 136 us,
-// 5.2 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 248 us, 4.8 TB/s.
+// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 136 to 140
+// us, 5.1 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 250, 4.8 TB/s.
 // The scales are a word for each row and column of a tile, so that planes and
 // scales of 485 MB are 533 MB of lines in the gradient. Giving each XCD an
 // eighth of all tiles, in bands of 2 to 64 rows of tiles, would bring more of
