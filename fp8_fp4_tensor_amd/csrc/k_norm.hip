@@ -332,7 +332,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 512 ? 4 : 1) void k_r
 }
 
 // dw = the sum of n rows of partial sums: 32 columns a workgroup, 32 rows at a
-// time, each thread's rows in order and then the 32 threads of a column.
+// time, each thread's rows in order and then the 32 threads of a column, as a
+// tree: one after the other they would round 31 times a sum that is nearly whole.
 __global__ __launch_bounds__(kWG) void k_rmsnorm_dw(NormBackArgs a, int n)
 {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -348,11 +349,17 @@ __global__ __launch_bounds__(kWG) void k_rmsnorm_dw(NormBackArgs a, int n)
     __syncthreads();
     if (rg > 0 || c >= a.cols)
         return;
+    f32x4 t[32];
 #pragma unroll
-    for (int i = 1; i < 32; ++i)
-        sum += part[i][cg];
+    for (int i = 0; i < 32; ++i)
+        t[i] = part[i][cg];
+#pragma unroll
+    for (int half = 16; half >= 1; half /= 2)
+#pragma unroll
+        for (int i = 0; i < half; ++i)
+            t[i] += t[i + half];
     f32x4* to = (f32x4*)(a.dw + c);
-    *to = a.acc ? *to + sum : sum;
+    *to = a.acc ? *to + t[0] : t[0];
 }
 
 // Workgroups of the gradient's kernel: two a CU, or one that takes four rows
