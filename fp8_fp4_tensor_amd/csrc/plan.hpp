@@ -224,6 +224,16 @@ inline MxPlan plan_gemm_mx(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bo
     return best;
 }
 
+// ---------------------------------------------------------------- planes
+// Bytes that a store of a tile's MX scales takes at a time: a row's (column's)
+// `codes` of them start at code `first` of a row of `per`, and each store has to
+// lie on its own size. The second half of a gated activation's gradient starts
+// at any code.
+constexpr int scale_store_bytes(int64_t per, int64_t first, int codes)
+{
+    return codes != 4 ? 1 : ((per | first) & 3) == 0 ? 4 : ((per | first) & 1) == 0 ? 2 : 1;
+}
+
 // ---------------------------------------------------------------- attention
 constexpr int kAttnStep = 64;     // keys a step of a wave takes
 constexpr int kAttnRows = 16;     // query rows of a workgroup of the kernel for few rows

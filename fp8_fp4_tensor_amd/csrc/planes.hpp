@@ -9,6 +9,7 @@
 
 #include "codec.hpp"
 #include "launch.hpp"
+#include "plan.hpp"
 
 namespace fq {
 
@@ -247,6 +248,29 @@ __device__ __forceinline__ void row_scales(const float (&v)[8][4], TileLds& lds,
         mult[i] = lds.row_mult[threadIdx.x >> 3][i];
 }
 
+// A tile's scales of one row of a plane with `per` scales a row: `codes` E8M0
+// codes, or one fp32, from scale `first` on.
+template <bool MX>
+__device__ __forceinline__ void store_scales(void* plane, int64_t row, int64_t per, int64_t first, int codes, uint32_t word)
+{
+    const int64_t at = row * per + first;
+    if constexpr (!MX) {
+        ((uint32_t*)plane)[at] = word;
+    } else {
+        uint8_t* to = (uint8_t*)plane + at;
+        switch (scale_store_bytes(per, first, codes)) {
+        case 4: *(uint32_t*)to = word; break;
+        case 2:
+            ((uint16_t*)to)[0] = (uint16_t)word;
+            ((uint16_t*)to)[1] = (uint16_t)(word >> 16);
+            break;
+        default:
+            for (int j = 0; j < codes; ++j)
+                to[j] = (uint8_t)(word >> 8 * j);
+        }
+    }
+}
+
 // Planes of a tile's values: the rowwise one if q, the colwise one (codes of
 // X^T [C, R], whole lines of 128 bytes) if qt. Every thread calls it; a second
 // tile may follow at once.
@@ -307,17 +331,8 @@ __device__ __forceinline__ void tile_planes(const float (&v)[8][4], TileLds& lds
     }
     lds_barrier();
     if (q && threadIdx.x < t.rows) {
-        const int64_t per = C / T::kBlock;
-        const int64_t at = (t.r0 + threadIdx.x) * per + t.c0 / T::kBlock;
-        const uint32_t word = lds.row_scale[threadIdx.x];
-        if constexpr (!T::kMx) {
-            ((uint32_t*)s)[at] = word;
-        } else if (t.cols == kTileSide && (per & 3) == 0) {
-            *(uint32_t*)((uint8_t*)s + at) = word;
-        } else {
-            for (int j = 0; j < t.cols / 32; ++j)
-                ((uint8_t*)s)[at + j] = (uint8_t)(word >> 8 * j);
-        }
+        const int64_t per = C / T::kBlock, first = t.c0 / T::kBlock;
+        store_scales<T::kMx>(s, t.r0 + threadIdx.x, per, first, t.cols / 32, lds.row_scale[threadIdx.x]);
     }
     if (!qt)
         return;
@@ -366,17 +381,8 @@ __device__ __forceinline__ void tile_planes(const float (&v)[8][4], TileLds& lds
             st16_stream(qt + (t.c0 + col) * pitch + (kPacked ? t.r0 / 2 : t.r0) + ch * 16, ld16(lds.codes + tile_at(col, ch)));
     }
     if (threadIdx.x < t.cols) {
-        const int64_t per = R / T::kBlock;
-        const int64_t at = (t.c0 + threadIdx.x) * per + t.r0 / T::kBlock;
-        const uint32_t word = lds.scale[threadIdx.x];
-        if constexpr (!T::kMx) {
-            ((uint32_t*)st)[at] = word;
-        } else if (t.rows == kTileSide && (per & 3) == 0) {
-            *(uint32_t*)((uint8_t*)st + at) = word;
-        } else {
-            for (int j = 0; j < t.rows / 32; ++j)
-                ((uint8_t*)st)[at + j] = (uint8_t)(word >> 8 * j);
-        }
+        const int64_t per = R / T::kBlock, first = t.r0 / T::kBlock;
+        store_scales<T::kMx>(st, t.c0 + threadIdx.x, per, first, t.rows / 32, lds.scale[threadIdx.x]);
     }
 }
 
