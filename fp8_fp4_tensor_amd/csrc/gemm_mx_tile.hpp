@@ -26,8 +26,6 @@
 namespace fq {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 template <int FA, int FB, bool WIDE, int TM, int TN, int WM, int WN, int NS, int S>
 struct MxTile {
     static constexpr bool kBoth4 = FA == kE2M1 && FB == kE2M1;
@@ -101,17 +99,6 @@ struct MxFrag {
     }
 };
 
-template <int S>
-struct MxAcc;
-template <>
-struct MxAcc<16> {
-    typedef f32x4 T;
-};
-template <>
-struct MxAcc<32> {
-    typedef f32x16 T;
-};
-
 template <int FR, int FC, int S, int OPSEL>
 __device__ __forceinline__ typename MxAcc<S>::T mfma_scaled(i32x8 r, uint32_t rs, i32x8 c, uint32_t cs, typename MxAcc<S>::T acc)
 {
@@ -121,15 +108,6 @@ __device__ __forceinline__ typename MxAcc<S>::T mfma_scaled(i32x8 r, uint32_t rs
     else
         return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(r, c, acc, kMfmaType<FR>, kMfmaType<FC>, OPSEL, (int)rs,
                                                                OPSEL, (int)cs);
-}
-
-template <int S>
-__device__ __forceinline__ typename MxAcc<S>::T mfma_bf16(bf16x8 r, bf16x8 c, typename MxAcc<S>::T acc)
-{
-    if constexpr (S == 16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(r, c, acc, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(r, c, acc, 0, 0, 0);
 }
 
 // A workgroup's tiles. Workgroups go to the eight XCDs round robin and each XCD
@@ -345,6 +323,99 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
             }
         }
     };
+    // Sums that are infinite or no numbers where the scales of a row of A or of B can be the cause (see add_block): they are
+    // noted, left out when the others are stored, and then, when the sums' registers are free, added up again. In code of
+    // its own, one sum after the other: what the ordinary way pays is a look at some sums (14336x4096x8160: 736 us with and
+    // without; a branch around each store of the ordinary way cost 8).
+    constexpr int E = S * S / 64;  // sums of a lane in an instruction's tile
+    constexpr int kWords = WIDE ? (NT * MT * E + 31) / 32 : 1;
+    uint32_t again[kWords];
+    const int64_t nb = g.k >> 5;
+    const int64_t block0 = (int64_t)first * (T::kStep / 32), block1 = min((int64_t)last * (T::kStep / 32), nb);
+    // this lane's row of row tile u of A, of column tile t of B; rows past the last repeat it and are not stored
+    auto row_of_a = [&](const MxSpan& s, int u) { return min(s.m0 + wm * (TM / WM) + u * S + row, g.m - 1); };
+    auto row_of_b = [&](const MxSpan& s, int t) { return min(s.n0 + wn * (TN / WN) + t * S + row, g.n - 1); };
+    auto note_beyond = [&](const MxSpan& s) -> bool {
+#pragma unroll
+        for (int y = 0; y < kWords; ++y)
+            again[y] = 0;
+        // An infinite value leaves no finite sum in its whole row (column): those of one column tile's first column and of one
+        // row tile tell. NaN if one is not finite; four chains, for each addition waits for the one before.
+        float zeros[4] = {};
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            zeros[u % 4] = __builtin_fmaf(acc[0][u][0], 0.0f, zeros[u % 4]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                zeros[e % 4] = __builtin_fmaf(acc[t][0][e], 0.0f, zeros[e % 4]);
+        const float zero = (zeros[0] + zeros[1]) + (zeros[2] + zeros[3]);
+        if (__ballot(zero != 0.0f) == 0)
+            return false;
+        uint32_t far_a = 0, far_b = 0;  // a bit for each of this lane's rows
+#pragma unroll 1
+        for (int u = 0; u < MT; ++u)
+            far_a |= past_top<FA, S>(g.sa + row_of_a(s, u) * nb, block0, block1, grp) ? 1u << u : 0u;
+#pragma unroll 1
+        for (int t = 0; t < NT; ++t)
+            far_b |= past_top<FB, S>(g.sb + row_of_b(s, t) * nb, block0, block1, grp) ? 1u << t : 0u;
+        if (__ballot((far_a | far_b) != 0) == 0)
+            return false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t far = far_a >> u | __shfl(far_b, row_of_sum<S>(e, grp)) >> t;
+                    const int bit = (t * MT + u) * E + e;
+                    again[bit / 32] |= (far & 1) && no_number(acc[t][u][e]) ? 1u << bit % 32 : 0u;
+                }
+        return true;
+    };
+    auto put_one = [&](const MxSpan& s, int t, int u, int e, float v) {
+        const int64_t i = s.m0 + wm * (TM / WM) + u * S + row, j = s.n0 + wn * (TN / WN) + t * S + row_of_sum<S>(e, grp);
+        if (i >= g.m || j >= g.n)
+            return;
+        float* to = (x.out == kOutPart ? x.part + (int64_t)blockIdx.y * g.m * g.n : (float*)g.c) + i * g.n + j;
+        *to = x.out != kOutPart && g.acc ? *to + v : v;
+    };
+    auto store_others = [&](const MxSpan& s) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int bit = (t * MT + u) * E + e;
+                    if ((again[bit / 32] >> bit % 32 & 1) == 0)
+                        put_one(s, t, u, e, acc[t][u][e]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+    };
+    auto add_beyond = [&](const MxSpan& s) {
+#pragma unroll 1
+        for (int q = 0; q < NT * MT; ++q) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int y = 0; y < kWords; ++y)
+                bits = q * E / 32 == y ? again[y] >> q * E % 32 : bits;
+            bits &= (1u << E) - 1;
+            if (__ballot(bits != 0) == 0)
+                continue;
+            const int64_t i = row_of_a(s, q % MT), j = row_of_b(s, q / MT);
+            const uint8_t *pa = g.a + mx_bytes<FA>(i * g.k), *pb = g.b + mx_bytes<FB>(j * g.k);
+            Acc sum{};
+#pragma unroll 1
+            for (int64_t b = block0; b < block1; ++b)
+                add_block<FA, FB, S>(pa, g.sa + i * nb, pb, g.sb + j * nb, b, grp, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (bits >> e & 1)
+                    put_one(s, q / MT, q % MT, e, sum[e]);
+        }
+    };
     auto store = [&](const MxSpan& s) {
         // A lane has, of row i, four consecutive columns from 4 grp on (S = 16), or four from 8 q + 4 grp on for q < 4.
 #pragma unroll
@@ -401,6 +472,16 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
                     }
             }
         }
+    };
+    auto put = [&](const MxSpan& s) {
+        if constexpr (WIDE) {
+            if (note_beyond(s)) {
+                store_others(s);
+                add_beyond(s);
+                return;
+            }
+        }
+        store(s);
     };
     if constexpr (kHalves) {
         // Steps run on from one tile to the next. A step's last products
@@ -473,7 +554,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
                         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(IA + IB) : "memory");
                 }
             }
-            store(span);
+            put(span);
             if (!more)
                 break;
             span = next;
@@ -516,7 +597,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
             here = here + 1 == NS ? 0 : here + 1;
             there = there + 1 == NS ? 0 : there + 1;
         }
-        store(span);
+        put(span);
     }
 }
 

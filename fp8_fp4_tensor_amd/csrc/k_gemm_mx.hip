@@ -78,6 +78,26 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_gemm_mx_few(GemmMxArgs a)
             }
         }
     }
+    if constexpr (WIDE) {
+        // as in the tiles: this wave's sums that are not finite, where a row's scales can be the cause
+        float zero = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            zero = __builtin_fmaf(acc[e], 0.0f, zero);
+        if (__ballot(zero != 0.0f) != 0) {
+            const int far_a = past_top<FA, 16>(psa, 0, nb, g), far_b = past_top<FB, 16>(psb, 0, nb, g);
+            if (__ballot((far_a | far_b) != 0) != 0) {
+                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int64_t b0 = 8 * w; b0 < nb; b0 += 8 * kFewWaves)
+                    for (int64_t b = b0; b < min(b0 + 8, nb); ++b)
+                        add_block<FA, FB, 16>(pa, psa, pb, psb, b, g, sum);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((far_a | __shfl(far_b, row_of_sum<16>(e, g))) && no_number(acc[e]))
+                        acc[e] = sum[e];
+            }
+        }
+    }
     part[w][lane] = acc;
     __syncthreads();
     if (w > 0 || m0 + row >= a.m)
@@ -251,6 +271,7 @@ hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t st)
     rest.g.m = g.m - p.main;
     rest.g.a += (g.fa == kE2M1 ? p.main * g.k / 2 : p.main * g.k);
     rest.sa += p.main * x.words;
+    rest.g.sa += p.main * (g.k / 32);
     rest.g.c = (char*)g.c + p.main * g.n * (g.bf ? 2 : 4);
     const hipError_t e = part(x, 0, 1, st);
     return e == hipSuccess ? part(rest, p.kind, p.splits, st) : e;

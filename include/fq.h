@@ -594,8 +594,10 @@ fq_status fq_attention(const fq_kv_cache *cache, const fq_kv_batch *batch, const
  * on both sides and bf16 outputs the matrix instruction keeps each product to
  * about 2^-12 of the largest of its 128 (1.5e-5 of the result in the mean
  * square, against 2^-9 for the output's rounding). fp32 outputs have products
- * and sums in fp32 throughout; there a value below 2^-126 in magnitude may
- * count as zero.
+ * and sums in fp32 throughout; there a value (code times scale) below 2^-126 in
+ * magnitude may count as zero. Values beyond fp32's largest count as what they
+ * are on either side, with either result (tiles of fp32 results that meet such values
+ * take up to ten times as long); a result is infinite where the product is.
  *   accumulate   1: C += the product (FQ_IN_F32 only), 0: C = the product.
  *   k % 32 == 0; m*k, n*k and m*n at most 2^36, k at most 2^22, m and n at most 2^28.
  * k = 0 gives zeros (or leaves C with accumulate); m = 0 or n = 0 does nothing.
