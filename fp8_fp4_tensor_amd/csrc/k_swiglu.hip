@@ -5,7 +5,7 @@
 //
 // Nothing crosses rows or columns but the blocks' scales, so a 128x128 tile is
 // read once and leaves as rowwise and colwise planes. With e = exp(-g), s is
-// 1 / (1 + e) and 1 - s is e s, neither of which cancels. The hardware's base-2
+// 1 / (1 + e) and 1 - s is e s where the difference would cancel. The hardware's base-2
 // exponential and its reciprocal are off by a unit in the last place each; the
 // exponent's rounding, which would add 2^-24 |g| log2(e), and the error of its
 // constant are taken back to first order, and the reciprocal refined once: s is
@@ -39,7 +39,8 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& rest)
     const float e = __builtin_fmaf(p, __builtin_fmaf(a, -kLo, __builtin_fmaf(a, -kHi, -t)) * 0.693147181f, p);
     const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     s = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-    rest = e * s;
+    // The gradient's 1 + gate (1 - s) cancels around a gate of -1.28: there the difference is the one that is off by least.
+    rest = g < 0.0f ? 1.0f - s : e * s;
 }
 
 // One value: y, or with BACK dgate and dup.

@@ -15,7 +15,8 @@ U = 2.0 ** -23
 # What that leaves: the second order of the exponent's rounding, (87 log2(e) 2^-24)^2 / 2, and its constant's error in two
 # fp32 terms, 87 * 2^-49: below 0.01 units each.
 # s = 1 / (1 + e): e's share of 1 + e at most, half a unit of the sum and half of the refined reciprocal: 2.5.
-# 1 - s = e s: 1.5 + 2.5 + 0.5 = 4.5. Each product adds half. Products of these errors stay below 0.1 units in all.
+# 1 - s: e s for positive gates, 1.5 + 2.5 + 0.5 = 4.5; less for the others, see the test of the cancelling slope. Each product
+# adds half. Products of these errors stay below 0.1 units in all.
 S, REST = 2.5, 4.5
 
 
@@ -57,6 +58,24 @@ def test_activation_counts_its_roundings(planes):
                                        (S + 1.5 + 0.1) * np.abs(slope) + REST * np.abs(g * rest) + 0.5 * np.abs(slope)))):
         err, bound = np.abs(got - want), U * units + t
         assert np.all(err <= bound), (name, (err / bound).max(), g[(err / bound).argmax()])
+
+
+@pytest.mark.parametrize("planes", [False, True], ids=["rows", "tiles"])
+def test_slope_where_it_cancels(planes):
+    """1 + gate (1 - s) is zero at a gate of -1.2785. There 1 - s is a difference: it is off by s's own error, of e's 1.5
+    units the share 1 - s and the sum's and the reciprocal's halves, and by half a unit of [1/2, 1)."""
+    rng = np.random.default_rng(5)
+    n = 1 << 20
+    gate = rng.uniform(-1.4, -1.15, n).astype(np.float32)
+    one = np.ones(n, np.float32)
+    _, dgate, _ = run(gate, one, one, 256, planes)
+    g = gate.astype(np.float64)
+    s, rest = B.sigmoid(g), B.sigmoid(-g)
+    slope = 1 + g * rest
+    off = s * (1.5 * rest + 1.0) + 0.25
+    bound = U * s * (np.abs(g) * off + (S + 1.5 + 0.1) * np.abs(slope)) * 1.01
+    err = np.abs(dgate - s * slope)
+    assert np.all(err <= bound), ((err / bound).max(), g[(err / bound).argmax()])
 
 
 def test_sigmoid_in_the_mean_square():
