@@ -14,13 +14,13 @@
 // result (8192x14336: a microsecond). Where exp(-|g|) is no normal number
 // it counts as zero: gates beyond 87.
 //
-// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 136 to 140
-// us, 5.1 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 250, 4.8 TB/s.
+// Bytes bound it. 8192x14336 in bf16 with both planes 8-bit: 712 MB in 138 us,
+// 5.1 TB/s (a large copy reaches 5.05); its gradient 1.19 GB in 243 to 250, 4.8 TB/s.
 // The scales are a word for each row and column of a tile, so that planes and
 // scales of 485 MB are 533 MB of lines in the gradient. Giving each XCD an
 // eighth of all tiles, in bands of 2 to 64 rows of tiles, would bring more of
 // them together, but moves the times by 10% either way with the pitch of the rows (bands
-// of 16: 135 and 231 us here, 94 and 157 for 8192x8192 where runs take 80 and 137).
+// of 16: 135 and 231 us here, 94 and 157 for 8192x8192; tile_in_turn has the times of what is done).
 #include <algorithm>
 
 #include "launch.hpp"
@@ -137,8 +137,9 @@ constexpr int kKept = 6;
 // The tile of turn t. Consecutive workgroups go to the eight XCDs in turn; a
 // run of eight neighbouring tiles goes to one of them instead, whose L2 then
 // has whole pieces of the rows and of their scales. The order of the whole stays
-// the rows' own. (8192x14336 139 and 244 us, 146 and 254 without; 8192x8192 80
-// and 137, 83 and 146; runs of 2, 4, 16 and 32 in between or the same.)
+// the rows' own. (The activation and its gradient in one call, when this was
+// chosen: 8192x14336 139 and 244 us, 146 and 254 without; 8192x8192 80 and 137,
+// 83 and 146; runs of 2, 4, 16 and 32 in between or the same.)
 __device__ __forceinline__ int64_t tile_in_turn(int64_t t, int64_t tiles)
 {
     constexpr uint32_t kRun = 8;

@@ -139,15 +139,17 @@ struct MxPlan {
 // bytes at 6.3 TB/s, the longer and a quarter of the other, plus the join of
 // shares. Measured both ways, what is chosen first (us; 8-bit both sides and
 // bf16 results where nothing is said):
-//   1x4096x4096        few rows 5.6, 64x64 in 8 shares 7.2
-//   16x8192x8192       64x64 in 4 shares 14.9, few rows 23.8
-//   16x18432x7168      64x128 in 3 shares 31.4, whole 39.7
-//   48x18432x7168      64x128 in 3 shares 37.4, whole 43.8; 4-bit 21.3 and 20.1
-//   256x4096x4096      64x64 14.7, 64x128 18.4
-//   1003x7168x2048     128x256 21.5, 256x256 27.1, 64x128 28.1
-//   512x4096x14336     128x256 in 4 shares 48.3, 256x256 in 6 50.6, 64x128 56.7
-//   4096x4096x4096     256x256 59.5, 128x256 72.6; 4-bit 42.9 and 50.1; fp32 103 and 120
-//   14336x4096x8192    fp32: three rounds of 256x256 and the rest on 128x256 700, all on 256x256 702, on 128x256 769
+//   1x4096x4096        few rows 7.5, 64x64 in 8 shares 7.1; 4-bit B 4.3 and 6.8
+//   16x8192x8192       64x128 in 8 shares 16.0, 64x64 in 4 15.0, few rows 23.8
+//   16x18432x7168      64x128 in 3 shares 31.4, in 8 31.2
+//   48x18432x7168      64x128 in 3 shares 37.4, 128x256 in 3 38.9; 4-bit 21.3, whole 19.7
+//   256x4096x4096      64x64 14.7, 64x128 18.3
+//   1003x7168x2048     128x256 21.7, 256x256 27.5, 64x128 28.0
+//   512x4096x14336     128x256 in 4 shares 48.2, 256x256 in 6 51.1, 64x128 57.1
+//   4096x4096x4096     256x256 59, 128x256 73; 4-bit 42.5 and 50.7; fp32 104 and 119
+//   14336x4096x8192    fp32: three rounds of 256x256 and the rest on 128x256 697, all on 256x256 703, on 128x256 771
+// Over 130 shapes the choice takes 4.0% longer than the best (geometric mean), at worst 1.35 times as long (20x8848x3840,
+// 4-bit, fp32 results: 64x128 in 6 shares 12.3, 64x64 9.1).
 inline MxPlan plan_gemm_mx_part(int64_t m, int64_t n, int64_t k, bool a4, bool b4, bool bf)
 {
     MxPlan best;
@@ -156,8 +158,9 @@ inline MxPlan plan_gemm_mx_part(int64_t m, int64_t n, int64_t k, bool a4, bool b
     constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
     const double bytes = (double)m * (a4 ? k / 2 : k) + (double)n * (b4 ? k / 2 : k) + (double)(m + n) * k / 32 +
                          (double)m * n * (bf ? 2 : 4);
-    // few rows, and a workgroup of k_gemm_mx_few a CU or little of B: one launch and no LDS
-    // (12x9104x1152, 4-bit: 3.6 us, 64x64 4.7; 1x14336x4096, 4-bit B: 11.2, 64x64 in 2 shares 11.8)
+    // few rows, and a workgroup of k_gemm_mx_few a CU or little of B: one launch and no LDS (12x9104x1152, 4-bit: 3.6
+    // us, 64x64 4.7). The border is not exact: beyond it 1x14336x4096 with 4-bit B takes 14.1 (64x128 in 16 shares) and
+    // few rows 11.3, 7x7616x7424 in 4 bits 11.6 and 9.7; within it 2x1112x16256 with 4-bit B 10.2, 64x64 in 12 shares 8.8.
     if (m <= 16 && ((n <= 4096 && k <= 16384) || (double)n * (b4 ? k / 2 : k) <= 9e6))
         return best;
     for (int t = 0; t < kMxTileKinds; ++t) {

@@ -646,7 +646,8 @@ fq_status fq_gemm_mx(const fq_gemm_mx_desc *desc, const fq_plane *a, const fq_pl
  * to nearest even, no transform; rows and cols those of the norm; rowwise, colwise or
  * both. in_dtype, seed, offset and rht_signs are not read.
  * At least one of y and the planes is asked for; both lie apart from all other
- * tensors. The sum of a row's squares must be finite in fp32.
+ * tensors. The sum of a row's squares must be finite in fp32; squares
+ * below 2^-126 may lose digits (which an eps of 2^-100 or more covers).
  */
 typedef struct {
     int64_t rows, cols;
@@ -689,7 +690,9 @@ fq_status fq_rmsnorm_backward(const fq_rmsnorm_desc *desc, const void *h, const 
  *   y         [rows, cols] of y_dtype, or NULL
  *   planes, out   as for fq_rmsnorm, of [rows, cols]
  *   cols % 8 == 0, cols <= 2^28, 2*rows*cols <= 2^36; x_stride a multiple of 8
- *   (bf16) or 4. x finite.
+ *   (bf16) or 4. x finite. y lies apart from x, the planes from all other tensors.
+ * s = 1 / (1 + exp(-g)) is off by 2.5 units in the last place at most; below
+ * 2^-126 (gates below -87) it counts as zero.
  */
 typedef struct {
     int64_t rows, cols;
@@ -707,7 +710,7 @@ fq_status fq_swiglu(const fq_swiglu_desc *desc, const fq_desc *planes, const voi
  *   dy    [rows, cols] of y_dtype
  *   dx    [rows, 2 * cols] of x_dtype, contiguous: dgate, then dup; or NULL. It
  *         may be x, if that is contiguous: each element is read before it is
- *         written.
+ *         written. Otherwise it lies apart from x, and always from dy.
  *   planes, out   of the fp32 dx, [rows, 2 * cols] (planes->cols = 2 * cols,
  *                 cols a multiple of the block)
  */
