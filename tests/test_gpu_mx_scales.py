@@ -55,6 +55,20 @@ def test_values_beyond_fp32_on_one_side(kind, tile, split, rest, arranged, shape
             check(out, reference(values(*a, fa), values(*b, fb)), k, fa, fb, False, f"{fa} {fb} {shape}")
 
 
+@pytest.mark.parametrize("kind,shape", [e for e in EVERY if e[0] != "widened"], ids=name)
+def test_far_scales_of_bf16_results(kind, shape):
+    """The same with bf16 results, whose instruction takes the scales as they are."""
+    m, n, k = shape
+    for fa, fb in P.KINDS[kind][0]:
+        a, b = operand(m, k, fa, 11), operand(n, k, fb, 12)
+        a[1][::3, 0], b[1][:, 0] = 250, 20
+        b[1][::2, -1], a[1][:, -1] = 250, 20
+        out = result(m, n, True)
+        call(a, b, fa, fb, out)
+        torch.cuda.synchronize()
+        check(out, reference(values(*a, fa), values(*b, fb)), k, fa, fb, True, f"{fa} {fb} {shape}")
+
+
 @pytest.mark.parametrize("shape", [(5, 131, 416), (33, 66, 320), (563, 65, 4032), (67, 2818, 5760), (16440, 387, 128)], ids=name)
 def test_other_rows_and_columns_stay_as_they_are(shape):
     """Rows of A and columns of B whose values are beyond fp32's range change no bit of the others, sums of which lie in the
