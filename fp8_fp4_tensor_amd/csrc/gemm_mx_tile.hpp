@@ -325,20 +325,10 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
     };
     // Sums that are infinite or no numbers where the scales of a row of A or of B can be the cause (see add_block): they are
     // noted, left out when the others are stored, and then, when the sums' registers are free, added up again. In code of
-    // its own, one sum after the other: what the ordinary way pays is a look at some sums (14336x4096x8160: 736 us with and
-    // without; a branch around each store of the ordinary way cost 8).
+    // its own, one sum after the other: what the ordinary way pays is a look at some sums (4096x4096x4096, 8-bit: 109.2 us,
+    // 108.7 without; a branch around each store of the ordinary way would cost 1%).
     constexpr int E = S * S / 64;  // sums of a lane in an instruction's tile
-    constexpr int kWords = WIDE ? (NT * MT * E + 31) / 32 : 1;
-    uint32_t again[kWords];
-    const int64_t nb = g.k >> 5;
-    const int64_t block0 = (int64_t)first * (T::kStep / 32), block1 = min((int64_t)last * (T::kStep / 32), nb);
-    // this lane's row of row tile u of A, of column tile t of B; rows past the last repeat it and are not stored
-    auto row_of_a = [&](const MxSpan& s, int u) { return min(s.m0 + wm * (TM / WM) + u * S + row, g.m - 1); };
-    auto row_of_b = [&](const MxSpan& s, int t) { return min(s.n0 + wn * (TN / WN) + t * S + row, g.n - 1); };
-    auto note_beyond = [&](const MxSpan& s) -> bool {
-#pragma unroll
-        for (int y = 0; y < kWords; ++y)
-            again[y] = 0;
+    auto not_finite = [&]() {
         // An infinite value leaves no finite sum in its whole row (column): those of one column tile's first column and of one
         // row tile tell. NaN if one is not finite; four chains, for each addition waits for the one before.
         float zeros[4] = {};
@@ -351,17 +341,42 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
             for (int e = 0; e < E; ++e)
                 zeros[e % 4] = __builtin_fmaf(acc[t][0][e], 0.0f, zeros[e % 4]);
         const float zero = (zeros[0] + zeros[1]) + (zeros[2] + zeros[3]);
-        if (__ballot(zero != 0.0f) == 0)
-            return false;
+        return __ballot(zero != 0.0f) != 0;
+    };
+    // Stores all sums and returns true, or false if none of the scales is that large.
+    auto store_beyond = [&](const MxSpan& s) {
+        // What it takes is loaded and computed here: kept since the kernel's start it would change the steps' registers and
+        // with them the order of their instructions (256x4096x4096 23.1 us, 22.4 so, 22.0 without all of this).
+        typedef const MxTileArgs __attribute__((address_space(4))) * Kernarg;
+        Kernarg at = (Kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+        int thread = threadIdx.x;
+        asm volatile("" : "+s"(at), "+v"(thread));
+        const uint8_t *ga = at->g.a, *gb = at->g.b, *gsa = at->g.sa, *gsb = at->g.sb;
+        const int64_t m = at->g.m, n = at->g.n, k = at->g.k, nb = k >> 5;
+        const bool part = at->out == kOutPart, add = !part && at->g.acc;
+        float* const to = part ? at->part + (int64_t)blockIdx.y * m * n : (float*)at->g.c;
+        const int lane = thread & 63, w = __builtin_amdgcn_readfirstlane(thread >> 6), row = lane % S, grp = lane / S;
+        const int64_t i0 = s.m0 + w / WN * (TM / WM), j0 = s.n0 + w % WN * (TN / WN);
+        const int64_t block0 = (int64_t)first * (T::kStep / 32), block1 = min((int64_t)last * (T::kStep / 32), nb);
+        // this lane's row of row tile u of A, of column tile t of B; rows past the last repeat it and are not stored
+        auto row_of_a = [&](int u) { return min(i0 + u * S + row, m - 1); };
+        auto row_of_b = [&](int t) { return min(j0 + t * S + row, n - 1); };
         uint32_t far_a = 0, far_b = 0;  // a bit for each of this lane's rows
 #pragma unroll 1
         for (int u = 0; u < MT; ++u)
-            far_a |= past_top<FA, S>(g.sa + row_of_a(s, u) * nb, block0, block1, grp) ? 1u << u : 0u;
+            far_a |= past_top<FA, S>(gsa + row_of_a(u) * nb, block0, block1, grp) ? 1u << u : 0u;
 #pragma unroll 1
         for (int t = 0; t < NT; ++t)
-            far_b |= past_top<FB, S>(g.sb + row_of_b(s, t) * nb, block0, block1, grp) ? 1u << t : 0u;
+            far_b |= past_top<FB, S>(gsb + row_of_b(t) * nb, block0, block1, grp) ? 1u << t : 0u;
         if (__ballot((far_a | far_b) != 0) == 0)
             return false;
+        auto put_one = [&](int t, int u, int e, float v) {
+            const int64_t i = i0 + u * S + row, j = j0 + t * S + row_of_sum<S>(e, grp);
+            if (i < m && j < n)
+                to[i * n + j] = add ? to[i * n + j] + v : v;
+        };
+        constexpr int kWords = (NT * MT * E + 31) / 32;
+        uint32_t again[kWords] = {};
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -370,31 +385,12 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
                 for (int e = 0; e < E; ++e) {
                     const uint32_t far = far_a >> u | __shfl(far_b, row_of_sum<S>(e, grp)) >> t;
                     const int bit = (t * MT + u) * E + e;
-                    again[bit / 32] |= (far & 1) && no_number(acc[t][u][e]) ? 1u << bit % 32 : 0u;
-                }
-        return true;
-    };
-    auto put_one = [&](const MxSpan& s, int t, int u, int e, float v) {
-        const int64_t i = s.m0 + wm * (TM / WM) + u * S + row, j = s.n0 + wn * (TN / WN) + t * S + row_of_sum<S>(e, grp);
-        if (i >= g.m || j >= g.n)
-            return;
-        float* to = (x.out == kOutPart ? x.part + (int64_t)blockIdx.y * g.m * g.n : (float*)g.c) + i * g.n + j;
-        *to = x.out != kOutPart && g.acc ? *to + v : v;
-    };
-    auto store_others = [&](const MxSpan& s) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int u = 0; u < MT; ++u)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int bit = (t * MT + u) * E + e;
-                    if ((again[bit / 32] >> bit % 32 & 1) == 0)
-                        put_one(s, t, u, e, acc[t][u][e]);
+                    if ((far & 1) && no_number(acc[t][u][e]))
+                        again[bit / 32] |= 1u << bit % 32;
+                    else
+                        put_one(t, u, e, acc[t][u][e]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-    };
-    auto add_beyond = [&](const MxSpan& s) {
 #pragma unroll 1
         for (int q = 0; q < NT * MT; ++q) {
             uint32_t bits = 0;
@@ -404,17 +400,18 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
             bits &= (1u << E) - 1;
             if (__ballot(bits != 0) == 0)
                 continue;
-            const int64_t i = row_of_a(s, q % MT), j = row_of_b(s, q / MT);
-            const uint8_t *pa = g.a + mx_bytes<FA>(i * g.k), *pb = g.b + mx_bytes<FB>(j * g.k);
+            const int64_t i = row_of_a(q % MT), j = row_of_b(q / MT);
+            const uint8_t *pa = ga + mx_bytes<FA>(i * k), *pb = gb + mx_bytes<FB>(j * k);
             Acc sum{};
 #pragma unroll 1
             for (int64_t b = block0; b < block1; ++b)
-                add_block<FA, FB, S>(pa, g.sa + i * nb, pb, g.sb + j * nb, b, grp, sum);
+                add_block<FA, FB, S>(pa, gsa + i * nb, pb, gsb + j * nb, b, grp, sum);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (bits >> e & 1)
-                    put_one(s, q / MT, q % MT, e, sum[e]);
+                    put_one(q / MT, q % MT, e, sum[e]);
         }
+        return true;
     };
     auto store = [&](const MxSpan& s) {
         // A lane has, of row i, four consecutive columns from 4 grp on (S = 16), or four from 8 q + 4 grp on for q < 4.
@@ -474,13 +471,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gemm_mx_tile(MxTileArgs x)
         }
     };
     auto put = [&](const MxSpan& s) {
-        if constexpr (WIDE) {
-            if (note_beyond(s)) {
-                store_others(s);
-                add_beyond(s);
+        if constexpr (WIDE)
+            if (__builtin_expect(not_finite(), 0) && store_beyond(s))
                 return;
-            }
-        }
         store(s);
     };
     if constexpr (kHalves) {
